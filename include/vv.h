@@ -179,6 +179,168 @@ vv_status vv_lm_head_argmax(const float* x, const uint16_t* gamma, const uint16_
                             void* ws, size_t ws_bytes, vv_stream stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * A batch that continues one shared prompt ([STATUS]: several contexts stepped alongside each
+ * other; [BITNET] decoder_init / decoder_step).  Several transcripts of one recording, or several
+ * questions about it, decode together from the prompt that one vv_decoder_init_seq (or any other
+ * prefill) left in a contiguous cache slice [Hkv, cap, D]; what each sequence adds lives in pages
+ * of a common pool.  A step of such a batch, per layer, with the caller's projections between:
+ *   vv_paged_plan      once a step: pages, slots, positions and row offsets of the new tokens
+ *   vv_qk_rope_append  per layer: head norms, rotation, keys and values into their pages
+ *   vv_gqa_prefix_attn per layer: attention over the shared prompt and the sequence's pages
+ *   vv_logits_process  once a step: penalties, biases, grammar mask, greedy token per row
+ * All of them are asynchronous on `stream`, allocate nothing, and may be captured into CUDA
+ * graphs; pointers are fixed at capture, lengths are read on the device at replay.  Element types
+ * are VV_F16, VV_BF16 and VV_F32.
+ */
+#define VV_F16 0
+#define VV_BF16 1
+#define VV_F32 2
+
+/* A pool of key/value pages: element d of token t (0 <= t < page_size) of head h in page p lies
+ * at p * page_stride + h * head_stride + t * token_stride + d (strides in elements, multiples of
+ * 8; the same for K and V).  Both [pages, Hkv, page_size, D] and [pages, page_size, Hkv, D] are
+ * such layouts.  Slot number = page * page_size + t. */
+typedef struct vv_paged_kv {
+  void* k;              /* device, 16-byte aligned */
+  void* v;
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t token_stride;
+  int32_t pages;        /* pages in the pool; pages * page_size < 2^31 */
+  int32_t page_size;    /* tokens per page: a multiple of 16 */
+  int32_t dtype;        /* VV_F16 or VV_BF16 */
+} vv_paged_kv;
+
+/* Block tables and slot map of a step, from the requests' lengths.
+ *   request b has lens[b] tokens in its pages and appends new_lens[b] (0 is allowed);
+ *   old = ceil(lens / page_size), need = ceil((lens + new) / page_size): the need - old new pages
+ *   of the requests are taken from free_pages in request order, starting at *cursor;
+ *   block_tables[b, old .. need-1] receives them (other entries are left as they are);
+ *   lens_out[b] = lens[b] + new_lens[b];  offsets[b] = sum of new_lens before b, offsets[B] = all;
+ *   token j of request b is row offsets[b] + j: slots = table[b, i / page_size] * page_size +
+ *   i % page_size and positions = prefix_len + i with i = lens[b] + j;
+ *   rows offsets[B] .. max_tokens-1 are padding: slot -1, position 0;
+ *   *cursor_out = *cursor + pages taken.
+ * lens, new_lens device int32 [B]; free_pages device int32 [n_free] (may be NULL when n_free is
+ * 0); cursor device int32 [1] or NULL (0); block_tables device int32 [B, max_blocks]; lens_out
+ * device int32 [B]; offsets device int32 [B + 1]; slots device int64 [max_tokens]; positions
+ * device int32 [max_tokens]; cursor_out device int32 [1].  Pages are numbers in [0, pages).
+ * lens_out and cursor_out must not overlap lens, new_lens and cursor.  page_size >= 1 (any),
+ * 1 <= B <= 16384.
+ * On the device: a negative length, one whose position would pass 2^31 - 1, or a page number
+ * outside [0, pages) records VV_ERR_RANGE; more new tokens than max_tokens, more pages than
+ * free_pages holds or a table longer than max_blocks records VV_ERR_CAPACITY (vv_sync_status
+ * reports either).  Nothing out of bounds is then read or written; tokens without a page get
+ * slot -1, table entries without one -1, rows past max_tokens are dropped, and a request with a
+ * bad length appends nothing.
+ * Errors: VV_ERR_INVALID_ARG, VV_ERR_SHAPE. */
+vv_status vv_paged_plan(const int32_t* lens, const int32_t* new_lens, int32_t B,
+                        int32_t prefix_len, int32_t page_size, int32_t pages,
+                        const int32_t* free_pages, int32_t n_free, const int32_t* cursor,
+                        int32_t* block_tables, int32_t max_blocks, int32_t* lens_out,
+                        int32_t* offsets, int64_t* slots, int32_t* positions, int32_t max_tokens,
+                        int32_t* cursor_out, vv_stream stream);
+
+/* Head norms, rotary position and cache write of T projected tokens, in one pass:
+ *   q, k heads: x <- x / sqrt(mean(x^2) + eps) * gain when a gain is given;
+ *   then (x_i, x_{i+D/2}) <- (x_i c - x_{i+D/2} s, x_{i+D/2} c + x_i s), c and s the cosine and
+ *   sine of positions[t] * theta^(-2i/D) (rotate-half; any int32 position);
+ *   q goes to q_out, k and v to slot slots[t] of the pool.
+ * q [T, Hq, D], k and v [T, Hkv, D] of kv->dtype: heads of a token contiguous, rows q_stride /
+ * k_stride / v_stride elements apart (multiples of 8: the three parts of one fused projection can
+ * be read in place); q_gain, k_gain device [D] of kv->dtype or NULL; positions device int32 [T];
+ * slots device int64 [T]; q_out [T, Hq, D] with rows q_out_stride apart, q itself (same stride)
+ * or apart from it.  A negative slot writes no key and value (padding); its q row is rotated all
+ * the same.  Slots of one call must differ (else which token a cell keeps is not defined).
+ * Arithmetic in fp32, angles reduced in fp64, one rounding at the end; v is copied.
+ * Requirements: D == 128, 1 <= Hq, Hkv <= 1024, 1 <= T < 2^31.  On the device, a slot past the
+ * pool records VV_ERR_RANGE and writes nothing.
+ * Errors: VV_ERR_INVALID_ARG, VV_ERR_SHAPE. */
+vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, int64_t T, int32_t Hq, int32_t Hkv,
+                            int32_t D, const void* q_gain, const void* k_gain, float eps,
+                            const int32_t* positions, float theta, const int64_t* slots,
+                            const vv_paged_kv* kv, void* q_out, int64_t q_out_stride,
+                            vv_stream stream);
+
+/* Grouped-query attention of one token per sequence over a shared prompt and its own pages:
+ *   out[b, h] = softmax over t (scale * q[b, h] . K[t]) . V,  keys = the prompt's prefix_len
+ *   positions, then own_lens[b] tokens in the pages of block_tables[b]; head h reads key-value
+ *   head h / (Hq / Hkv).  The prompt's scores are computed for all sequences together.
+ * q [B, Hq, D] of kv->dtype, rows q_stride elements apart; k_prefix, v_prefix [Hkv, prefix_len, D]
+ * of the same type with the given strides (elements, multiples of 8), e.g. one layer's slice of a
+ * decoder's cache (NULL when prefix_len is 0); block_tables device int32 [B, max_blocks], only
+ * the entries that own_lens reaches are read; own_lens device int32 [B]; out [B, Hq, D], rows
+ * out_stride apart; lse device fp32 [B, Hq] or NULL: log of the sum of exp(score).
+ * A sequence without any key (or with every score -inf) gives zeros and lse -inf; own_lens[b] < 0
+ * marks a padding row: its q is not used and its rows of out and lse are left as they were.
+ * Scores, softmax and sums in fp32; the weights are rounded to the element type before they meet
+ * V (as 2^x of at most 2^8: a relative half step each).
+ * ws: device workspace of vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, D, prefix_len,
+ * max_blocks * page_size) bytes, 16-byte aligned, zero-filled once before its first use and left
+ * ready by every call; calls sharing one ws (captured ones included) must not overlap on the GPU.
+ * Requirements: D == 128, Hq % Hkv == 0, Hq / Hkv <= 16, 1 <= B <= 65535, 1 <= Hkv <= 1024,
+ * 0 <= prefix_len < 2^24, max_blocks >= 1, scale positive and finite, 16-byte aligned pointers.
+ * On the device, a page number outside [0, pages) records VV_ERR_RANGE and its keys are left
+ * out; an own_lens past max_blocks * page_size records VV_ERR_CAPACITY and is cut there.
+ * Errors: VV_ERR_INVALID_ARG, VV_ERR_SHAPE, VV_ERR_CAPACITY (ws too small). */
+size_t vv_gqa_prefix_attn_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                         int32_t prefix_len, int64_t max_own);
+vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t B, int32_t Hq, int32_t Hkv,
+                             int32_t D, const void* k_prefix, const void* v_prefix,
+                             int64_t prefix_head_stride, int64_t prefix_token_stride,
+                             int32_t prefix_len, const vv_paged_kv* kv,
+                             const int32_t* block_tables, int32_t max_blocks,
+                             const int32_t* own_lens, float scale, void* out, int64_t out_stride,
+                             float* lse, void* ws, size_t ws_bytes, vv_stream stream);
+
+/* Penalties, biases and a grammar's mask on a batch of logits, and the greedy token of each row.
+ * With n the number of times token v occurs in the row's generated part and `seen` whether it
+ * occurs in its prompt or generated part, in this order (fp32, each operation rounded once):
+ *   seen:    x <- x > 0 ? x / repetition[b] : x * repetition[b]
+ *   n > 0:   x <- (x - frequency[b] * n) - presence[b]
+ *   bias:    x <- x + bias value of (b, v)
+ *   mask bit 0: x <- -inf
+ * then out[b, v] = x rounded to the logits' type and argmax[b] = the lowest v whose x (before
+ * that rounding) is the largest; NaN is never chosen; -1 when no x is above -inf. */
+typedef struct vv_logits_rules {
+  const int32_t* tokens;       /* device [B, >= token_lens], rows tokens_stride apart: the prompt's
+                                  ids, then the generated ones; NULL: no history */
+  int64_t tokens_stride;
+  const int32_t* token_lens;   /* device [B]: ids in the row (prompt and generated) */
+  const int32_t* prompt_lens;  /* device [B]: how many of them are the prompt's; NULL: 0 */
+  int32_t max_tokens;          /* token_lens are at most this (the width of `tokens`) */
+  const float* repetition;     /* device fp32 [B] (> 0) or NULL: no such penalty */
+  const float* frequency;      /* device fp32 [B] or NULL */
+  const float* presence;       /* device fp32 [B] or NULL */
+  const int32_t* bias_ids;     /* device [n_bias]: row b owns entries bias_offsets[b] ..
+                                  bias_offsets[b + 1] - 1; an id named twice keeps its last value;
+                                  NULL: no biases */
+  const float* bias_vals;      /* device fp32 [n_bias] */
+  const int32_t* bias_offsets; /* device [B + 1], ascending */
+  int32_t n_bias;
+  const uint32_t* mask;        /* device [B, ceil(V / 32)], rows mask_stride words apart: bit
+                                  v % 32 of word v / 32 set = v is allowed; NULL: all are */
+  int64_t mask_stride;
+} vv_logits_rules;
+
+/* logits and out: device [B, V] of `dtype` (VV_F32, VV_F16 or VV_BF16), rows the given number of
+ * elements apart; out may be the logits themselves (same stride), else it must not overlap them.
+ * argmax device int32 [B] or NULL.  Ids outside [0, V) in tokens and bias_ids are passed over
+ * (padding); lengths outside [0, max_tokens] and offsets outside [0, n_bias] are cut to that
+ * range, and record VV_ERR_RANGE.
+ * ws (used with argmax only, else may be NULL): device workspace of
+ * vv_logits_process_workspace_size(B) bytes, 16-byte aligned, zero-filled once before its first
+ * use and left zero by every call; calls sharing one ws (captured ones included) must not overlap
+ * on the GPU.
+ * Requirements: 1 <= B <= 65535, 1 <= V < 2^30, max_tokens < 2^24.
+ * Errors: VV_ERR_INVALID_ARG, VV_ERR_SHAPE, VV_ERR_CAPACITY. */
+size_t vv_logits_process_workspace_size(int32_t B);
+vv_status vv_logits_process(const void* logits, int64_t logits_stride, int32_t dtype, int32_t B,
+                            int64_t V, const vv_logits_rules* rules, void* out, int64_t out_stride,
+                            int32_t* argmax, void* ws, size_t ws_bytes, vv_stream stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Decoder ([BITNET] decoder_init / decoder_step contracts; [ASR] "Highlights": KV cache kept
  * resident on the GPU, step replayed as one CUDA graph instead of ~1950 launches).
  *

@@ -6,9 +6,11 @@ there is no fallback of any kind, and importing this module fails loudly when li
 been built.
 """
 
+import contextlib
 import ctypes
 import os
 import re
+from collections import namedtuple
 from ctypes import POINTER, Structure, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import torch
@@ -29,6 +31,10 @@ VV_TERNARY = 1
 VV_KV_F16 = 0
 VV_KV_BF16 = 1
 VV_KV_F32 = 2
+VV_F16 = 0
+VV_BF16 = 1
+VV_F32 = 2
+DTYPES = {torch.float16: VV_F16, torch.bfloat16: VV_BF16, torch.float32: VV_F32}
 
 
 class VVError(RuntimeError):
@@ -61,6 +67,20 @@ class vv_model_weights(Structure):
                 ("layers", POINTER(vv_layer_weights))]
 
 
+class vv_paged_kv(Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("page_stride", c_int64),
+                ("head_stride", c_int64), ("token_stride", c_int64), ("pages", c_int32),
+                ("page_size", c_int32), ("dtype", c_int32)]
+
+
+class vv_logits_rules(Structure):
+    _fields_ = [("tokens", c_void_p), ("tokens_stride", c_int64), ("token_lens", c_void_p),
+                ("prompt_lens", c_void_p), ("max_tokens", c_int32), ("repetition", c_void_p),
+                ("frequency", c_void_p), ("presence", c_void_p), ("bias_ids", c_void_p),
+                ("bias_vals", c_void_p), ("bias_offsets", c_void_p), ("n_bias", c_int32),
+                ("mask", c_void_p), ("mask_stride", c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -82,6 +102,19 @@ def _load():
                                            c_float, P, P]),
         "vv_lm_head_argmax_workspace_size": (c_size_t, [c_int64]),
         "vv_lm_head_argmax": (S, [P, P, P, c_int64, c_int64, c_float, P, P, P, c_size_t, P]),
+        "vv_paged_plan": (S, [P, P, c_int32, c_int32, c_int32, c_int32, P, c_int32, P, P, c_int32,
+                              P, P, P, P, c_int32, P, P]),
+        "vv_qk_rope_append": (S, [P, c_int64, P, c_int64, P, c_int64, c_int64, c_int32, c_int32,
+                                  c_int32, P, P, c_float, P, c_float, P, POINTER(vv_paged_kv), P,
+                                  c_int64, P]),
+        "vv_gqa_prefix_attn_workspace_size": (c_size_t, [c_int32, c_int32, c_int32, c_int32,
+                                                         c_int32, c_int64]),
+        "vv_gqa_prefix_attn": (S, [P, c_int64, c_int32, c_int32, c_int32, c_int32, P, P, c_int64,
+                                   c_int64, c_int32, POINTER(vv_paged_kv), P, c_int32, P, c_float,
+                                   P, c_int64, P, P, c_size_t, P]),
+        "vv_logits_process_workspace_size": (c_size_t, [c_int32]),
+        "vv_logits_process": (S, [P, c_int64, c_int32, c_int32, c_int64, POINTER(vv_logits_rules),
+                                  P, c_int64, P, P, c_size_t, P]),
         "vv_decoder_create": (S, [POINTER(vv_config), POINTER(vv_model_weights), P, P,
                                   POINTER(c_void_p)]),
         "vv_decoder_destroy": (S, [P]),
@@ -237,3 +270,281 @@ def vv_lm_head_argmax(x, gamma, w_lm, eps, ws, logits=True, stream=None):
     check(lib.vv_lm_head_argmax(ptr(x), ptr(gamma), ptr(w_lm), V, H, eps, ptr(lg), ptr(idx),
                                 ptr(ws), ws.numel() * ws.element_size(), stream_handle(stream)))
     return lg, idx
+
+
+# --------------------------------------------------------- a batch that continues one shared prompt
+# These entry points take tensors of any device (all of one call on the same one): the call runs
+# with that device current, on `stream` or on the device's current torch stream, and the tensors it
+# makes are made on that stream.  A tensor of the wrong type, shape, layout or device is a VVError
+# (VV_ERR_INVALID_ARG), raised before anything is launched.
+def _refuse(text):
+    raise VVError(VV_ERR_INVALID_ARG, text)
+
+
+def _same(device, who, **tensors):
+    """Every given tensor lives on `device` (a CUDA one)."""
+    if device.type != "cuda":
+        _refuse(f"{who}: tensors must be on a CUDA device, got {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            _refuse(f"{who}: {name} is on {t.device}, expected {device}")
+
+
+def _dense(who, dtype, **tensors):
+    """Every given (name=(tensor, shape)) is contiguous, of `dtype` and `shape` (None: any)."""
+    for name, (t, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype or not t.is_contiguous():
+            _refuse(f"{who}: {name} must be contiguous {dtype}, got {t.dtype}, strides {t.stride()}")
+        if shape is not None and tuple(t.shape) != shape:
+            _refuse(f"{who}: {name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _rows(who, name, t, dtype, last):
+    """`t` is [rows, ...] of `dtype` whose trailing dimensions `last` are contiguous in a row;
+    returns the row stride in elements."""
+    if t.dtype != dtype:
+        _refuse(f"{who}: {name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 + len(last) or tuple(t.shape[1:]) != last:
+        _refuse(f"{who}: {name} has shape {tuple(t.shape)}, expected [rows, {', '.join(map(str, last))}]")
+    want = 1
+    for size, stride in zip(reversed(last), reversed(t.stride()[1:])):
+        if size > 1 and stride != want:
+            _refuse(f"{who}: the rows of {name} must be contiguous, strides {t.stride()}")
+        want *= size
+    return t.stride(0) if t.shape[0] > 1 else want
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+_here = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Context in which `device` and `stream` (None: its current one) are current."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _here
+    return _switched(device, stream)
+
+
+class PagedKV:
+    """A pool of key/value pages for vv_qk_rope_append and vv_gqa_prefix_attn.
+
+    k, v: fp16 or bf16 tensors [pages, Hkv, page_size, 128] of equal strides, the last dimension
+    contiguous; a pool laid out [pages, page_size, Hkv, 128] is passed as k.transpose(1, 2)."""
+
+    def __init__(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            _refuse("PagedKV: k and v must be 4-dimensional, of one shape, layout and type")
+        if k.dtype not in (torch.float16, torch.bfloat16):
+            _refuse(f"PagedKV: fp16 or bf16 pages, got {k.dtype}")
+        if k.stride(3) != 1 and k.shape[3] > 1:
+            _refuse("PagedKV: the last dimension must be contiguous")
+        _same(k.device, "PagedKV", v=v)
+        self.k, self.v = k, v
+        self.pages, self.heads, self.page_size, self.head_dim = k.shape
+        self.dtype, self.device = k.dtype, k.device
+        self.c = vv_paged_kv(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
+                             self.pages, self.page_size, DTYPES[k.dtype])
+        self.ref = ctypes.byref(self.c)
+
+
+PagedPlan = namedtuple("PagedPlan", "lens offsets slots positions cursor")
+
+
+def vv_paged_plan(lens, new_lens, block_tables, free_pages, page_size, pages, max_tokens,
+                  prefix_len=0, cursor=None, out=None, stream=None):
+    """Pages, slots and positions of a step's new tokens.
+
+    lens, new_lens int32 [B]; block_tables int32 [B, max_blocks], updated in place; free_pages
+    int32 [n] of page numbers in [0, pages), taken from index *cursor (int32 [1], None: 0) on.
+    Returns PagedPlan(lens int32 [B], offsets int32 [B + 1], slots int64 [max_tokens], positions
+    int32 [max_tokens], cursor int32 [1]); `out` may give such a tuple to write into."""
+    who, dev, B = "vv_paged_plan", lens.device, lens.numel()
+    _same(dev, who, new_lens=new_lens, block_tables=block_tables, free_pages=free_pages,
+          cursor=cursor)
+    if block_tables.dim() != 2:
+        _refuse(f"{who}: block_tables must be [B, max_blocks]")
+    _dense(who, torch.int32, lens=(lens, (B,)), new_lens=(new_lens, (B,)),
+           block_tables=(block_tables, (B, block_tables.shape[1])),
+           free_pages=(free_pages, (free_pages.numel(),)), cursor=(cursor, (1,)))
+    with _on(dev, stream):
+        if out is None:
+            e = torch.empty
+            out = PagedPlan(e(B, dtype=torch.int32, device=dev),
+                            e(B + 1, dtype=torch.int32, device=dev),
+                            e(max_tokens, dtype=torch.int64, device=dev),
+                            e(max_tokens, dtype=torch.int32, device=dev),
+                            e(1, dtype=torch.int32, device=dev))
+        else:
+            out = PagedPlan(*out)
+            _same(dev, who, **out._asdict())
+            _dense(who, torch.int32, lens=(out.lens, (B,)), offsets=(out.offsets, (B + 1,)),
+                   positions=(out.positions, (max_tokens,)), cursor=(out.cursor, (1,)))
+            _dense(who, torch.int64, slots=(out.slots, (max_tokens,)))
+        check(lib.vv_paged_plan(lens.data_ptr(), new_lens.data_ptr(), B, prefix_len, page_size,
+                                pages, free_pages.data_ptr(), free_pages.numel(),
+                                None if cursor is None else cursor.data_ptr(),
+                                block_tables.data_ptr(), block_tables.shape[1],
+                                out.lens.data_ptr(), out.offsets.data_ptr(), out.slots.data_ptr(),
+                                out.positions.data_ptr(), max_tokens, out.cursor.data_ptr(),
+                                stream_handle(stream)))
+    return out
+
+
+def vv_qk_rope_append(q, k, v, positions, slots, kv, theta, q_gain=None, k_gain=None, eps=1e-6,
+                      stream=None, out=None):
+    """Head norms (where gains are given), rotation at `positions` and the write of k and v into
+    `kv` (a PagedKV) at `slots`; returns the rotated q.
+
+    q [T, Hq, 128], k, v [T, Hkv, 128] of the pool's type, rows may be strided; positions int32
+    [T]; slots int64 [T]; gains [128].  out: [T, Hq, 128], q itself allowed."""
+    who, dev, dt = "vv_qk_rope_append", q.device, kv.dtype
+    T, Hq, D = q.shape if q.dim() == 3 else _refuse(f"{who}: q must be [T, Hq, D]")
+    _same(dev, who, k=k, v=v, positions=positions, slots=slots, kv=kv, q_gain=q_gain,
+          k_gain=k_gain, out=out)
+    tail = (kv.heads, kv.head_dim)
+    if D != kv.head_dim or k.shape[0] != T or v.shape[0] != T:
+        _refuse(f"{who}: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, head dimension "
+                f"{kv.head_dim}")
+    qs, ks, vs = (_rows(who, "q", q, dt, (Hq, D)), _rows(who, "k", k, dt, tail),
+                  _rows(who, "v", v, dt, tail))
+    _dense(who, torch.int32, positions=(positions, (T,)))
+    _dense(who, torch.int64, slots=(slots, (T,)))
+    _dense(who, dt, q_gain=(q_gain, (D,)), k_gain=(k_gain, (D,)))
+    with _on(dev, stream):
+        o = out if out is not None else torch.empty((T, Hq, D), dtype=dt, device=dev)
+        os = _rows(who, "out", o, dt, (Hq, D))
+        if o.shape[0] != T:
+            _refuse(f"{who}: out has {o.shape[0]} rows, expected {T}")
+        check(lib.vv_qk_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq,
+                                    kv.heads, D, None if q_gain is None else q_gain.data_ptr(),
+                                    None if k_gain is None else k_gain.data_ptr(), eps,
+                                    positions.data_ptr(), theta, slots.data_ptr(), kv.ref,
+                                    o.data_ptr(), os, stream_handle(stream)))
+    return o
+
+
+def vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, D, prefix_len, max_own):
+    return lib.vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, D, prefix_len, max_own)
+
+
+def vv_gqa_prefix_attn(q, k_prefix, v_prefix, kv, block_tables, lens, scale, ws, stream=None,
+                       out=None, lse=None):
+    """Attention of one token per sequence over a shared prompt and the sequence's pages.
+
+    q [B, Hq, 128] (rows may be strided); k_prefix, v_prefix [Hkv, P, 128] or None; kv a PagedKV;
+    block_tables int32 [B, max_blocks]; lens int32 [B] (tokens in the pages; < 0: padding row);
+    ws: zero-filled once, vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, 128, P, max_blocks *
+    page_size) bytes.  Returns out [B, Hq, 128]; lse fp32 [B, Hq] receives the log sums."""
+    who, dev, dt = "vv_gqa_prefix_attn", q.device, kv.dtype
+    B, Hq, D = q.shape if q.dim() == 3 else _refuse(f"{who}: q must be [B, Hq, D]")
+    _same(dev, who, k_prefix=k_prefix, v_prefix=v_prefix, kv=kv, block_tables=block_tables,
+          lens=lens, ws=ws, out=out, lse=lse)
+    if D != kv.head_dim:
+        _refuse(f"{who}: q {tuple(q.shape)}, head dimension {kv.head_dim}")
+    if (k_prefix is None) != (v_prefix is None):
+        _refuse(f"{who}: k_prefix and v_prefix go together")
+    P, ph, pt, kp, vp = 0, 0, 0, None, None
+    if k_prefix is not None:
+        if (k_prefix.dim() != 3 or k_prefix.shape[0] != kv.heads or k_prefix.shape[2] != D or
+                v_prefix.shape != k_prefix.shape or v_prefix.stride() != k_prefix.stride() or
+                k_prefix.dtype != dt or v_prefix.dtype != dt or k_prefix.stride(2) != 1):
+            _refuse(f"{who}: k_prefix and v_prefix must be {dt} [{kv.heads}, P, {D}] of one layout, "
+                    "the last dimension contiguous")
+        P, ph, pt = k_prefix.shape[1], k_prefix.stride(0), k_prefix.stride(1)
+        if P < 2:
+            pt = max(pt, D)
+        kp, vp = k_prefix.data_ptr(), v_prefix.data_ptr()
+    if block_tables.dim() != 2:
+        _refuse(f"{who}: block_tables must be [B, max_blocks]")
+    blocks = block_tables.shape[1]
+    _dense(who, torch.int32, block_tables=(block_tables, (B, blocks)), lens=(lens, (B,)))
+    _dense(who, torch.float32, lse=(lse, (B, Hq)))
+    if not ws.is_contiguous():
+        _refuse(f"{who}: ws must be contiguous")
+    qs = _rows(who, "q", q, dt, (Hq, D))
+    with _on(dev, stream):
+        o = out if out is not None else torch.empty((B, Hq, D), dtype=dt, device=dev)
+        os = _rows(who, "out", o, dt, (Hq, D))
+        if o.shape[0] != B:
+            _refuse(f"{who}: out has {o.shape[0]} rows, expected {B}")
+        check(lib.vv_gqa_prefix_attn(q.data_ptr(), qs, B, Hq, kv.heads, D, kp, vp, ph, pt, P,
+                                     kv.ref, block_tables.data_ptr(), blocks, lens.data_ptr(),
+                                     scale, o.data_ptr(), os,
+                                     None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                                     ws.numel() * ws.element_size(), stream_handle(stream)))
+    return o
+
+
+def vv_logits_process_workspace_size(B):
+    return lib.vv_logits_process_workspace_size(B)
+
+
+def vv_logits_process(logits, ws=None, tokens=None, token_lens=None, prompt_lens=None,
+                      repetition=None, frequency=None, presence=None, bias_ids=None,
+                      bias_vals=None, bias_offsets=None, mask=None, argmax=True, stream=None,
+                      out=None):
+    """Penalties, biases and a bit mask on logits [B, V] (fp32, fp16 or bf16), and each row's
+    greedy token; returns (processed logits, int32 [B]) or (processed logits, None).
+
+    tokens int32 [B, W] (prompt, then generated ids), token_lens / prompt_lens int32 [B];
+    repetition, frequency, presence fp32 [B]; bias_ids int32 [n], bias_vals fp32 [n], bias_offsets
+    int32 [B + 1]; mask int32 [B, ceil(V / 32)], bit v % 32 of word v / 32 set = allowed.
+    ws (needed with argmax): zero-filled once, vv_logits_process_workspace_size(B) bytes.  out may
+    be logits itself."""
+    who, dev = "vv_logits_process", logits.device
+    if logits.dim() != 2 or logits.dtype not in DTYPES:
+        _refuse(f"{who}: logits must be fp32, fp16 or bf16 [B, V]")
+    B, V = logits.shape
+    _same(dev, who, ws=ws, tokens=tokens, token_lens=token_lens, prompt_lens=prompt_lens,
+          repetition=repetition, frequency=frequency, presence=presence, bias_ids=bias_ids,
+          bias_vals=bias_vals, bias_offsets=bias_offsets, mask=mask, out=out)
+    _dense(who, torch.int32, token_lens=(token_lens, (B,)), prompt_lens=(prompt_lens, (B,)),
+           bias_ids=(bias_ids, None), bias_offsets=(bias_offsets, (B + 1,)))
+    _dense(who, torch.float32, repetition=(repetition, (B,)), frequency=(frequency, (B,)),
+           presence=(presence, (B,)), bias_vals=(bias_vals, None))
+    r = vv_logits_rules()
+    if tokens is not None:
+        if token_lens is None or tokens.dim() != 2 or tokens.shape[0] != B:
+            _refuse(f"{who}: tokens must be [B, width] and come with token_lens")
+        r.tokens, r.max_tokens = tokens.data_ptr(), tokens.shape[1]
+        r.tokens_stride = _rows(who, "tokens", tokens, torch.int32, (tokens.shape[1],))
+        r.token_lens = token_lens.data_ptr()
+        for name, t in (("prompt_lens", prompt_lens), ("repetition", repetition),
+                        ("frequency", frequency), ("presence", presence)):
+            if t is not None:
+                setattr(r, name, t.data_ptr())
+    elif not (repetition is None and frequency is None and presence is None):
+        _refuse(f"{who}: penalties need tokens")
+    if bias_ids is not None:
+        if bias_vals is None or bias_offsets is None or bias_vals.numel() != bias_ids.numel():
+            _refuse(f"{who}: bias_ids, bias_vals and bias_offsets go together")
+        r.bias_ids, r.bias_vals = bias_ids.data_ptr(), bias_vals.data_ptr()
+        r.bias_offsets, r.n_bias = bias_offsets.data_ptr(), bias_ids.numel()
+    if mask is not None:
+        r.mask_stride = _rows(who, "mask", mask, torch.int32, ((V + 31) // 32,))
+        if mask.shape[0] != B:
+            _refuse(f"{who}: mask has {mask.shape[0]} rows, expected {B}")
+        r.mask = mask.data_ptr()
+    ls = _rows(who, "logits", logits, logits.dtype, (V,))
+    with _on(dev, stream):
+        o = out if out is not None else torch.empty((B, V), dtype=logits.dtype, device=dev)
+        os = _rows(who, "out", o, logits.dtype, (V,))
+        if o.shape[0] != B:
+            _refuse(f"{who}: out has {o.shape[0]} rows, expected {B}")
+        idx = torch.empty(B, dtype=torch.int32, device=dev) if argmax else None
+        if argmax and (ws is None or not ws.is_contiguous()):
+            _refuse(f"{who}: argmax needs a contiguous workspace")
+        check(lib.vv_logits_process(logits.data_ptr(), ls, DTYPES[logits.dtype], B, V,
+                                    ctypes.byref(r), o.data_ptr(), os,
+                                    idx.data_ptr() if argmax else None,
+                                    ws.data_ptr() if argmax else None,
+                                    ws.numel() * ws.element_size() if argmax else 0,
+                                    stream_handle(stream)))
+    return o, idx

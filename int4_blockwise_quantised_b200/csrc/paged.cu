@@ -1,0 +1,508 @@
+// Bookkeeping and key/value writes of a paged cache: vv_paged_plan and vv_qk_rope_append.
+//
+// Both belong to a batch that continues one shared prompt ("VibeVoice-1.5B — Current Status":
+// several contexts stepped alongside each other over the same weights): every sequence keeps its
+// own keys and values in pages of a common pool, vv_paged_plan hands out the pages and says
+// where each new token goes, vv_qk_rope_append puts it there.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "vv_device.cuh"
+#include "vv_internal.h"
+
+namespace vv {
+namespace {
+
+// ------------------------------------------------------------------------------------- plan
+//
+//   after_b = len_b + new_b          old_b = ceil(len_b / ps)     need_b = ceil(after_b / ps)
+//   table[b, old_b + j] = free[cursor + sum_{i<b} (need_i - old_i) + j]
+//   token j of request b: own index i = len_b + j, slot = table[b, i / ps] * ps + i % ps,
+//   position = prefix + i, row offsets[b] + j
+//
+// One launch and no communication between CTAs: each CTA scans all B requests itself (their
+// lengths are a few KB, in L2 after the first CTA), keeps the exclusive sums of tokens and pages
+// in shared memory and then takes its share of the requests, of the new pages and of the tokens;
+// a token or page finds its request by bisection in those sums.  A step of a small batch is one
+// CTA: what it costs is the latency of load, scan, bisection and store, not bytes.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxB = 16384;  // two int32 sums per request in shared memory
+
+struct PlanArgs {
+  const int32_t* lens;
+  const int32_t* news;
+  const int32_t* free_pages;
+  const int32_t* cursor;
+  int32_t* table;
+  int32_t* lens_out;
+  int32_t* offsets;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* cursor_out;
+  int B, prefix, ps, n_free, pool, max_blocks, max_tokens;
+};
+
+struct Request {
+  int len, add, old_blocks, fresh;
+};
+
+// A request's lengths; out-of-range ones count as no new token (`bad` is set).
+__device__ __forceinline__ Request load_request(const PlanArgs& a, int b, bool& bad) {
+  int len = a.lens[b], add = a.news[b];
+  if (len < 0 || add < 0 || (int64_t)len + add + a.prefix > 0x7fffffff) {
+    bad = true;
+    len = max(len, 0);
+    add = 0;
+  }
+  Request r;
+  r.len = len;
+  r.add = add;
+  const unsigned ps = (unsigned)a.ps;
+  r.old_blocks = (int)(((unsigned)len + ps - 1) / ps);
+  r.fresh = (int)(((unsigned)len + (unsigned)add + ps - 1) / ps) - r.old_blocks;
+  return r;
+}
+
+// Largest b in [0, n) with sums[b] <= x (sums ascending, sums[0] = 0).
+__device__ __forceinline__ int find_request(const int32_t* sums, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs a) {
+  extern __shared__ int32_t plan_smem[];
+  int32_t* tok0 = plan_smem;         // [B] exclusive sum of new tokens (saturated)
+  int32_t* page0 = plan_smem + a.B;  // [B] exclusive sum of new pages (saturated)
+  __shared__ int64_t warp_tok[kPlanThreads / 32], warp_page[kPlanThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int run = (a.B + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
+
+  bool bad = false;
+  int64_t nt = 0, np = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(a, b, bad);
+    nt += r.add;
+    np += r.fresh;
+  }
+  // block-wide exclusive scan in 64 bits (lengths come from the caller's device memory: their
+  // sum may pass 32 bits, which ends as a recorded error, not as a wrapped index)
+  int64_t st = nt, sp = np;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t ut = __shfl_up_sync(0xffffffffu, st, o), up = __shfl_up_sync(0xffffffffu, sp, o);
+    if (lane >= o) {
+      st += ut;
+      sp += up;
+    }
+  }
+  if (lane == 31) {
+    warp_tok[warp] = st;
+    warp_page[warp] = sp;
+  }
+  __syncthreads();
+  int64_t all_tok = 0, all_page = 0, t0 = 0, p0 = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w == warp) {
+      t0 = all_tok;
+      p0 = all_page;
+    }
+    all_tok += warp_tok[w];
+    all_page += warp_page[w];
+  }
+  t0 += st - nt;
+  p0 += sp - np;
+  const int cursor = a.cursor ? *a.cursor : 0;
+  const int64_t kSat = 0x7fffffff;
+  for (int b = b0; b < b1; ++b) {
+    bool dummy = false;
+    const Request r = load_request(a, b, dummy);
+    tok0[b] = (int32_t)min(t0, kSat);
+    page0[b] = (int32_t)min(p0, kSat);
+    t0 += r.add;
+    p0 += r.fresh;
+  }
+  __syncthreads();
+
+  int error = bad || cursor < 0 ? VV_ERR_RANGE : 0;
+  const int gtid = blockIdx.x * kPlanThreads + tid, gsize = gridDim.x * kPlanThreads;
+  const int n_tok = (int)min(all_tok, (int64_t)a.max_tokens);
+  if (all_tok > a.max_tokens) error = VV_ERR_CAPACITY;
+  if (gtid == 0) {
+    const int64_t end = (int64_t)cursor + all_page;
+    if (end > a.n_free) error = VV_ERR_CAPACITY;
+    *a.cursor_out = (int32_t)min(end, kSat);
+    a.offsets[a.B] = n_tok;
+  }
+  for (int b = gtid; b < a.B; b += gsize) {
+    bool dummy = false;
+    const Request r = load_request(a, b, dummy);
+    a.offsets[b] = min(tok0[b], n_tok);
+    a.lens_out[b] = r.len + r.add;
+  }
+  // the page of fresh index p (over all requests), -1 when the list has run out or names no page
+  auto fresh_page = [&](int64_t p) {
+    const int64_t at = p + cursor;
+    if (cursor < 0 || at >= a.n_free) return -1;
+    const int page = a.free_pages[at];
+    return page >= 0 && page < a.pool ? page : -1;
+  };
+  const int n_page = (int)min(all_page, (int64_t)kSat);
+  for (int p = gtid; p < n_page; p += gsize) {
+    const int b = find_request(page0, a.B, p);
+    const int block = ((unsigned)a.lens[b] + (unsigned)a.ps - 1) / (unsigned)a.ps + (p - page0[b]);
+    const int page = fresh_page(p);
+    if (block < a.max_blocks)
+      a.table[(int64_t)b * a.max_blocks + block] = page;
+    else
+      error = VV_ERR_CAPACITY;
+    if (page < 0 && error == 0) error = p + (int64_t)cursor >= a.n_free ? VV_ERR_CAPACITY : VV_ERR_RANGE;
+    if (gsize > 0x7fffffff - p) break;
+  }
+  // tokens, four in a row per thread: one bisection, then a walk
+  for (int64_t t4 = (int64_t)gtid * 4; t4 < a.max_tokens; t4 += (int64_t)gsize * 4) {
+    int64_t slot[4];
+    int pos[4];
+    int b = -1, end = -1, page = -1, blk = -1;
+    Request r = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = (int)t4 + e;
+      slot[e] = -1;
+      pos[e] = 0;
+      if (t >= n_tok) continue;
+      if (t >= end) {
+        if (b < 0) {
+          b = find_request(tok0, a.B, t);
+        } else {
+          do ++b;
+          while (b + 1 < a.B && tok0[b + 1] <= t);
+        }
+        bool dummy = false;
+        r = load_request(a, b, dummy);
+        end = (int)min((int64_t)tok0[b] + r.add, kSat);
+        blk = -1;
+      }
+      const int i = r.len + (t - tok0[b]);
+      const int block = (int)((unsigned)i / (unsigned)a.ps);
+      if (block != blk) {
+        blk = block;
+        if (block >= r.old_blocks) {
+          page = block < a.max_blocks ? fresh_page((int64_t)page0[b] + (block - r.old_blocks)) : -1;
+        } else {
+          page = block < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + block] : -1;
+          if (page < 0 || page >= a.pool) {
+            page = -1;
+            if (error == 0) error = block < a.max_blocks ? VV_ERR_RANGE : VV_ERR_CAPACITY;
+          }
+        }
+      }
+      if (page >= 0) slot[e] = (int64_t)page * a.ps + (i - block * a.ps);
+      pos[e] = a.prefix + i;
+    }
+    if (t4 + 4 <= a.max_tokens) {
+      longlong2* so = reinterpret_cast<longlong2*>(a.slots + t4);
+      so[0] = make_longlong2(slot[0], slot[1]);
+      so[1] = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + t4) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+      for (int e = 0; t4 + e < a.max_tokens; ++e) {
+        a.slots[t4 + e] = slot[e];
+        a.positions[t4 + e] = pos[e];
+      }
+    }
+  }
+  if (error) set_device_error(error);
+}
+
+// ------------------------------------------------------------------------------ rope append
+//
+//   x <- x / sqrt(mean(x^2) + eps) * gain            (query and key heads, when gains are given)
+//   (x_i, x_{i+64}) <- (x_i c - x_{i+64} s, x_{i+64} c + x_i s),  angle = pos * theta^(-2i/128)
+//
+// Bound by HBM: every head row is read once and written once (512 bytes for 128 elements, about
+// 30 floating operations per 4 bytes).  Half a warp holds one head row, 16 bytes a lane, so a
+// warp's load covers two rows; a lane's rotation partner is the lane 8 further on, and the squares
+// of a row are summed over its 16 lanes.  The angles of a token are found once per warp and
+// shared by all heads it handles: two frequencies a lane, the turns pos * theta^(-2i/128) / 2 pi
+// reduced to [-1/2, 1/2] in 64 bits (in 32 bits a position of 10^6 would lose the angle's second
+// digit), then sine and cosine of the remainder in 32 bits.
+constexpr int kHeadDim = 128;
+constexpr int kRopeWarps = 8;
+
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* kp;
+  void* vp;
+  const void* q_gain;
+  const void* k_gain;
+  const int32_t* pos;
+  const int64_t* slots;
+  int64_t q_stride, k_stride, v_stride, qo_stride;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t n_slots;
+  int T, Hq, Hkv, ps;
+  int pairs_per_unit, units_per_token;
+  float eps;
+  double turns[kHeadDim / 2];  // theta^(-2i/D) / (2 pi)
+};
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T, bool GAINS>
+__global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_append_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ float2 cs[kRopeWarps][kHeadDim / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t units = (int64_t)a.T * a.units_per_token;
+  const int heads = a.Hq + 2 * a.Hkv, pairs = (heads + 1) / 2;
+  const int c = lane & 15, row = lane >> 4;  // 16-byte chunk of the row; which row of the pair
+  const float sign = c < 8 ? -1.f : 1.f;
+  const double f0 = a.turns[lane], f1 = a.turns[lane + 32];
+  float qg[8], kg[8];
+  if (GAINS) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 one = make_float2(1.f, 1.f);
+      const float2 x = a.q_gain ? unpack2<T>(reinterpret_cast<const uint32_t*>(a.q_gain)[c * 4 + j]) : one;
+      const float2 y = a.k_gain ? unpack2<T>(reinterpret_cast<const uint32_t*>(a.k_gain)[c * 4 + j]) : one;
+      qg[2 * j] = x.x;
+      qg[2 * j + 1] = x.y;
+      kg[2 * j] = y.x;
+      kg[2 * j + 1] = y.y;
+    }
+  }
+  for (int64_t u = (int64_t)blockIdx.x * kRopeWarps + warp; u < units; u += (int64_t)gridDim.x * kRopeWarps) {
+    const int t = (int)(u / a.units_per_token);
+    const int first = (int)(u - (int64_t)t * a.units_per_token) * a.pairs_per_unit;
+    const int last = min(first + a.pairs_per_unit, pairs);
+    const double p = (double)a.pos[t];
+    const int64_t slot = a.slots[t];
+    bool write = slot >= 0;
+    if (slot >= a.n_slots) {
+      write = false;
+      if (lane == 0) set_device_error(VV_ERR_RANGE);
+    }
+    const int64_t page = write ? slot / a.ps : 0;
+    const int64_t cell = page * a.page_stride + (write ? slot - page * a.ps : 0) * a.token_stride;
+    __syncwarp();
+    {
+      const double x0 = p * f0, x1 = p * f1;
+      float s, co;
+      sincospif(2.f * (float)(x0 - rint(x0)), &s, &co);
+      cs[warp][lane] = make_float2(co, s);
+      sincospif(2.f * (float)(x1 - rint(x1)), &s, &co);
+      cs[warp][lane + 32] = make_float2(co, s);
+    }
+    __syncwarp();
+    float2 w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = cs[warp][(c & 7) * 8 + j];
+#pragma unroll 2
+    for (int pr = first; pr < last; ++pr) {
+      const int h = 2 * pr + row;
+      const bool live = h < heads;
+      const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+      const int hk = is_k ? h - a.Hq : h - a.Hq - a.Hkv;
+      const T* src = is_q ? static_cast<const T*>(a.q) + t * a.q_stride + h * kHeadDim
+                          : (is_k ? static_cast<const T*>(a.k) + t * a.k_stride
+                                  : static_cast<const T*>(a.v) + t * a.v_stride) + hk * kHeadDim;
+      uint4 in = make_uint4(0, 0, 0, 0);
+      if (live && (is_q || write)) in = *reinterpret_cast<const uint4*>(src + c * 8);
+      float x[8];
+      const uint32_t iw[4] = {in.x, in.y, in.z, in.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<T>(iw[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+      }
+      if (GAINS) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
+        const bool norm = is_q ? a.q_gain != nullptr : a.k_gain != nullptr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = norm ? x[j] * inv * (is_q ? qg[j] : kg[j]) : x[j];
+      }
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float other = __shfl_xor_sync(0xffffffffu, x[j], 8);
+        y[j] = fmaf(x[j], w[j].x, sign * other * w[j].y);
+      }
+      uint4 out = make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]),
+                             pack2<T>(y[6], y[7]));
+      if (!is_q && !is_k) out = in;
+      T* dst = is_q ? static_cast<T*>(a.q_out) + t * a.qo_stride + h * kHeadDim
+                    : static_cast<T*>(is_k ? a.kp : a.vp) + cell + hk * a.head_stride;
+      if (live && (is_q || write)) *reinterpret_cast<uint4*>(dst + c * 8) = out;
+    }
+  }
+}
+
+}  // namespace
+}  // namespace vv
+
+extern "C" vv_status vv_paged_plan(const int32_t* lens, const int32_t* new_lens, int32_t B,
+                                   int32_t prefix_len, int32_t page_size, int32_t pages,
+                                   const int32_t* free_pages, int32_t n_free,
+                                   const int32_t* cursor, int32_t* block_tables,
+                                   int32_t max_blocks, int32_t* lens_out, int32_t* offsets,
+                                   int64_t* slots, int32_t* positions, int32_t max_tokens,
+                                   int32_t* cursor_out, vv_stream stream) {
+  VV_CHECK_ARG(lens && new_lens && block_tables && lens_out && offsets && slots && positions &&
+                   cursor_out && (free_pages || n_free == 0),
+               "vv_paged_plan: null pointer");
+  VV_CHECK_ARG(vv::aligned16(slots) && vv::aligned16(positions),
+               "vv_paged_plan: slots and positions must be 16-byte aligned");
+  VV_CHECK_SHAPE(B >= 1 && B <= vv::kPlanMaxB, "vv_paged_plan: B=%d (1..%d)", B, vv::kPlanMaxB);
+  VV_CHECK_SHAPE(page_size >= 1 && pages >= 1 && (int64_t)pages * page_size < (int64_t(1) << 31),
+                 "vv_paged_plan: %d pages of %d tokens", pages, page_size);
+  VV_CHECK_SHAPE(prefix_len >= 0 && n_free >= 0 && max_blocks >= 1 && max_tokens >= 1 &&
+                     max_tokens <= 0x7ffffff0,
+                 "vv_paged_plan: prefix_len=%d n_free=%d max_blocks=%d max_tokens=%d", prefix_len,
+                 n_free, max_blocks, max_tokens);
+  // every CTA reads lens, new_lens and cursor while others write the outputs
+  auto apart = [](const void* a, size_t na, const void* b, size_t nb) {
+    const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+    return x + na <= y || y + nb <= x;
+  };
+  const size_t nb = (size_t)B * 4;
+  VV_CHECK_ARG(apart(lens, nb, lens_out, nb) && apart(new_lens, nb, lens_out, nb) &&
+                   (!cursor || apart(cursor, 4, cursor_out, 4)),
+               "vv_paged_plan: lens_out and cursor_out must not overlap lens, new_lens and cursor");
+  vv::PlanArgs a = {lens,  new_lens,   free_pages, cursor, block_tables, lens_out,
+                    offsets, slots, positions, cursor_out, B, prefix_len,
+                    page_size, n_free, pages, max_blocks, max_tokens};
+  const size_t smem = (size_t)B * 8;
+  if (smem > (48u << 10))
+    VV_CUDA(cudaFuncSetAttribute(vv::paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem));
+  // one CTA per 2048 tokens, at most one per SM (each repeats the scan)
+  const int64_t per = vv::kPlanThreads * 4;
+  const int grid = (int)std::min<int64_t>(vv::sm_count(), ((int64_t)max_tokens + per - 1) / per);
+  vv::paged_plan_kernel<<<grid, vv::kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+  return vv::cuda_check(cudaGetLastError(), "vv_paged_plan launch");
+}
+
+extern "C" vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride,
+                                       int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                       const void* q_gain, const void* k_gain, float eps,
+                                       const int32_t* positions, float theta,
+                                       const int64_t* slots, const vv_paged_kv* kv, void* q_out,
+                                       int64_t q_out_stride, vv_stream stream) {
+  VV_CHECK_ARG(q && k && v && positions && slots && kv && q_out, "vv_qk_rope_append: null pointer");
+  vv_status st = vv::check_paged_kv(kv, Hkv, D, "vv_qk_rope_append");
+  if (st != VV_OK) return st;
+  VV_CHECK_ARG(vv::aligned16(q) && vv::aligned16(k) && vv::aligned16(v) && vv::aligned16(q_out) &&
+                   vv::aligned16(q_gain) && vv::aligned16(k_gain),
+               "vv_qk_rope_append: pointers must be 16-byte aligned");
+  VV_CHECK_SHAPE(T >= 1 && T < (int64_t(1) << 31), "vv_qk_rope_append: T=%lld", (long long)T);
+  VV_CHECK_SHAPE(Hq >= 1 && Hq <= 1024, "vv_qk_rope_append: Hq=%d", Hq);
+  VV_CHECK_SHAPE(q_stride % 8 == 0 && k_stride % 8 == 0 && v_stride % 8 == 0 &&
+                     q_out_stride % 8 == 0 && q_stride >= 0 && k_stride >= 0 && v_stride >= 0 &&
+                     (T == 1 || q_out_stride >= (int64_t)Hq * D),
+                 "vv_qk_rope_append: row strides must be multiples of 8 elements and output rows "
+                 "must not overlap");
+  VV_CHECK_ARG(theta > 0.f && std::isfinite(theta) && eps >= 0.f && std::isfinite(eps),
+               "vv_qk_rope_append: theta=%g eps=%g", theta, eps);
+  // in place (same rows) or apart: a warp reads a whole head row before it writes it
+  const char* q0 = static_cast<const char*>(q);
+  const char* o0 = static_cast<const char*>(q_out);
+  const int64_t q_bytes = ((T - 1) * q_stride + (int64_t)Hq * D) * 2;
+  const int64_t o_bytes = ((T - 1) * q_out_stride + (int64_t)Hq * D) * 2;
+  VV_CHECK_ARG((q0 == o0 && (T == 1 || q_stride == q_out_stride)) || q0 + q_bytes <= o0 ||
+                   o0 + o_bytes <= q0,
+               "vv_qk_rope_append: q_out must be q itself (same stride) or not overlap it");
+  vv::RopeArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.kp = kv->k;
+  a.vp = kv->v;
+  a.q_gain = q_gain;
+  a.k_gain = k_gain;
+  a.pos = positions;
+  a.slots = slots;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.qo_stride = q_out_stride;
+  a.page_stride = kv->page_stride;
+  a.head_stride = kv->head_stride;
+  a.token_stride = kv->token_stride;
+  a.n_slots = (int64_t)kv->pages * kv->page_size;
+  a.T = (int)T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.ps = kv->page_size;
+  a.eps = eps;
+  // theta^(-2i/D) by repeated use of one logarithm in double: relative error of a few 2^-53
+  const double kTwoPi = 6.283185307179586476925286766559;
+  for (int i = 0; i < D / 2; ++i) a.turns[i] = std::pow((double)theta, -2.0 * i / D) / kTwoPi;
+  // a warp takes pairs_per_unit pairs of heads of one token: all of them when there are tokens
+  // enough for every warp slot, fewer when the batch is a step of a few tokens
+  const int pairs = (Hq + 2 * Hkv + 1) / 2;
+  const int64_t warps = (int64_t)vv::sm_count() * 32;
+  const int64_t per = std::max<int64_t>(1, std::min<int64_t>(pairs, T * pairs / warps));
+  a.pairs_per_unit = (int)per;
+  a.units_per_token = (int)((pairs + per - 1) / per);
+  const int64_t units = T * a.units_per_token;
+  const int grid = (int)std::min<int64_t>((units + vv::kRopeWarps - 1) / vv::kRopeWarps,
+                                          (int64_t)vv::sm_count() * 8);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool gains = q_gain || k_gain;
+  const dim3 block(vv::kRopeWarps * 32);
+  if (kv->dtype == VV_KV_F16) {
+    if (gains)
+      vv::qk_rope_append_kernel<__half, true><<<grid, block, 0, s>>>(a);
+    else
+      vv::qk_rope_append_kernel<__half, false><<<grid, block, 0, s>>>(a);
+  } else {
+    if (gains)
+      vv::qk_rope_append_kernel<__nv_bfloat16, true><<<grid, block, 0, s>>>(a);
+    else
+      vv::qk_rope_append_kernel<__nv_bfloat16, false><<<grid, block, 0, s>>>(a);
+  }
+  return vv::cuda_check(cudaGetLastError(), "vv_qk_rope_append launch");
+}

@@ -34,6 +34,26 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
     if (!(cond)) return ::vv::set_error(VV_ERR_SHAPE, __VA_ARGS__); \
   } while (0)
 
+// A page pool as vv_qk_rope_append and vv_gqa_prefix_attn take it: 16-bit elements, head dimension
+// 128, rows on 16-byte boundaries.
+inline vv_status check_paged_kv(const vv_paged_kv* kv, int Hkv, int D, const char* who) {
+  VV_CHECK_ARG(kv->k && kv->v && aligned16(kv->k) && aligned16(kv->v),
+               "%s: page pools null or not 16-byte aligned", who);
+  VV_CHECK_ARG(kv->dtype == VV_KV_F16 || kv->dtype == VV_KV_BF16, "%s: dtype %d (fp16 or bf16)",
+               who, kv->dtype);
+  VV_CHECK_SHAPE(D == 128, "%s: D=%d (only 128)", who, D);
+  VV_CHECK_SHAPE(Hkv >= 1 && Hkv <= 1024, "%s: Hkv=%d", who, Hkv);
+  VV_CHECK_SHAPE(kv->pages >= 1 && kv->page_size >= 16 && kv->page_size % 16 == 0 &&
+                     (int64_t)kv->pages * kv->page_size < (int64_t(1) << 31),
+                 "%s: %d pages of %d tokens (page size a multiple of 16)", who, kv->pages,
+                 kv->page_size);
+  VV_CHECK_SHAPE(kv->page_stride >= 0 && kv->head_stride >= 0 && kv->token_stride >= D &&
+                     kv->page_stride % 8 == 0 && kv->head_stride % 8 == 0 &&
+                     kv->token_stride % 8 == 0,
+                 "%s: page strides must be non-negative multiples of 8 elements", who);
+  return VV_OK;
+}
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 

@@ -19,6 +19,10 @@ What it computes, and where the pages fix it:
 * ``decoder``  — the ``decoder_step`` and ``decoder_init`` contracts of the
                  "vibevoice-asr-bitnet-onnx" model page (graph I/O listing), with the KV cache
                  stored in fp16 and everything else in float64.
+* ``batch``    — the operators of a batch that continues one shared prompt: block tables and slot
+                 maps, head norms with rotation and the paged cache write, attention over a shared
+                 prefix and own pages, penalties / biases / masks on logits (the contexts stepped
+                 alongside each other of "VibeVoice-1.5B — Current Status").
 
 The method reaches exactly (up to rounding order) the plain definition "dequantise, then dense
 matmul, then naive softmax attention", so this oracle is that definition written out. Each
@@ -26,4 +30,4 @@ reading taken where the pages are silent is stated in the docstring of the funct
 it. It shares no code with the CUDA path: it imports only numpy and the standard library.
 """
 
-from . import pack, ops, decoder  # noqa: F401
+from . import pack, ops, decoder, batch  # noqa: F401
