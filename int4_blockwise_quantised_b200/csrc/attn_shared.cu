@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "attn_shared.h"
 #include "vv_device.cuh"
 #include "vv_internal.h"
 
@@ -45,7 +46,7 @@ constexpr int kChunk = 16;                            // keys per chunk
 constexpr int kChunkBytes = kChunk * D * 2;           // K or V of a chunk
 constexpr int kStageBytes = 2 * kChunkBytes;
 constexpr int kMinChunks = 16;                        // least chunks of a split
-constexpr int kPart = D + 4;                          // floats of a partial row: o[128], m, l
+constexpr int kMinShared = 128;                       // least prompt with a kernel of its own
 
 struct SharedAttnArgs {
   const void* q;
@@ -57,8 +58,10 @@ struct SharedAttnArgs {
   const int32_t* lens;
   void* out;
   float* lse;
-  float* part;       // [B][Hkv][splits][G][kPart]
+  float* part;       // [B][Hkv][splits][G][kPartRow]: this kernel's parts
   unsigned* arrived; // [B][Hkv]
+  const float* pre_part;  // [Hkv][pre_splits][B * G][kPartRow]: the shared prompt's
+  int pre_splits;    // 0: the prompt's keys, if any, are read here (kpre, vpre, P)
   int64_t q_stride, out_stride, pre_head, pre_token, page_stride, head_stride, token_stride;
   int B, Hkv, G, P, ps, pages, max_blocks, splits;
   float c;  // scale * log2(e)
@@ -76,13 +79,6 @@ __device__ __forceinline__ uint32_t pack_pair<__nv_bfloat16>(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-template <typename T>
-__device__ __forceinline__ T round_to(float v);
-template <>
-__device__ __forceinline__ __half round_to<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
@@ -122,17 +118,23 @@ __global__ void __launch_bounds__(kOwnThreads) own_attn_kernel(const __grid_cons
   const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.G;
   const int raw_len = a.lens[b];
-  if (raw_len < 0) return;  // padding row
+  if (raw_len < 0) {  // padding row
+    pdl_wait();
+    return;
+  }
   const int cap = (int)min((int64_t)a.max_blocks * a.ps, (int64_t)0x7fffffff);
   const int len = min(raw_len, cap);
   if (raw_len > cap && tid == 0 && split == 0 && g == 0) set_device_error(VV_ERR_CAPACITY);
 
   // chunks: the prompt's first, then the sequence's own
-  const int npre = (a.P + kChunk - 1) / kChunk;
+  const int npre = a.pre_splits ? 0 : (a.P + kChunk - 1) / kChunk;
   const int nch = npre + (len + kChunk - 1) / kChunk;
   const int per = max((nch + a.splits - 1) / a.splits, kMinChunks);
   const int active = max((nch + per - 1) / per, 1);
-  if (split >= active) return;
+  if (split >= active) {
+    pdl_wait();
+    return;
+  }
   const int c0 = split * per, c1 = min(c0 + per, nch);
 
   const T* kpre = static_cast<const T*>(a.kpre) + (int64_t)g * a.pre_head;
@@ -307,12 +309,12 @@ __global__ void __launch_bounds__(kOwnThreads) own_attn_kernel(const __grid_cons
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
   }
-  float* sp = reinterpret_cast<float*>(osm);  // [warps][G][kPart]
+  float* sp = reinterpret_cast<float*>(osm);  // [warps][G][kPartRow]
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int row = (lane >> 2) + h * 8;
     if (row < G) {
-      float* d = sp + (warp * G + row) * kPart;
+      float* d = sp + (warp * G + row) * kPartRow;
 #pragma unroll
       for (int n = 0; n < 16; ++n)
         *reinterpret_cast<float2*>(d + n * 8 + (lane & 3) * 2) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
@@ -323,52 +325,69 @@ __global__ void __launch_bounds__(kOwnThreads) own_attn_kernel(const __grid_cons
     }
   }
   __syncthreads();
-  // thread = one dimension of every row
-  auto merge = [&](const float* parts, int n, int64_t stride, int row, float& M, float& L, float& O) {
-    M = -INFINITY;
-    for (int i = 0; i < n; ++i) M = fmaxf(M, parts[i * stride + (int64_t)row * kPart + D]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    L = 0.f;
-    O = 0.f;
-    for (int i = 0; i < n; ++i) {
-      const float* d = parts + i * stride + (int64_t)row * kPart;
-      const float w = exp2_fast(d[D] - ref);
-      L = fmaf(w, d[D + 1], L);
-      O = fmaf(w, d[tid], O);
+  // A warp joins a row at a time, four dimensions a lane.  Of each set of parts the maxima and sums
+  // are read 32 at a time, one a lane, then the rows one after the other: two round trips to L2
+  // for up to 32 parts.
+  struct Joined {
+    float m, l;
+    float4 o;
+  };
+  auto absorb = [&](Joined& r, const float* parts, int n, int64_t stride) {
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int cnt = min(n - i0, 32);
+      const float* base = parts + i0 * stride;
+      const float2 ml = lane < cnt ? *reinterpret_cast<const float2*>(base + lane * stride + D)
+                                   : make_float2(-INFINITY, 0.f);
+      const float mn = fmaxf(r.m, warp_max(ml.x)), ref = mn == -INFINITY ? 0.f : mn;
+      const float w0 = exp2_fast(r.m - ref), w = exp2_fast(ml.x - ref);
+      r.m = mn;
+      r.l = r.l * w0 + warp_sum(lane < cnt ? w * ml.y : 0.f);
+      r.o = make_float4(r.o.x * w0, r.o.y * w0, r.o.z * w0, r.o.w * w0);
+#pragma unroll 4
+      for (int i = 0; i < cnt; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float4 v = *reinterpret_cast<const float4*>(base + i * stride + lane * 4);
+        r.o = make_float4(fmaf(wi, v.x, r.o.x), fmaf(wi, v.y, r.o.y), fmaf(wi, v.z, r.o.z), fmaf(wi, v.w, r.o.w));
+      }
     }
   };
   const int64_t item = (int64_t)b * a.Hkv + g;
-  float* part = a.part + item * a.splits * G * kPart;
+  float* part = a.part + item * a.splits * G * kPartRow;
   if (active > 1) {
-    for (int row = 0; row < G; ++row) {
-      float M, L, O;
-      merge(sp, kOwnWarps, (int64_t)G * kPart, row, M, L, O);
-      float* d = part + ((int64_t)split * G + row) * kPart;
-      d[tid] = O;
-      if (tid == 0) {
-        d[D] = M;
-        d[D + 1] = L;
-      }
+    for (int row = warp; row < G; row += kOwnWarps) {
+      Joined r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      absorb(r, sp + row * kPartRow, kOwnWarps, (int64_t)G * kPartRow);
+      float* d = part + ((int64_t)split * G + row) * kPartRow;
+      *reinterpret_cast<float4*>(d + lane * 4) = r.o;
+      if (lane == 0) *reinterpret_cast<float2*>(d + D) = make_float2(r.m, r.l);
     }
     __threadfence();
     __syncthreads();
     if (tid == 0) s_last = atomicAdd(&a.arrived[item], 1u) == (unsigned)(active - 1);
     __syncthreads();
-    if (!s_last) return;
+    if (!s_last) {
+      pdl_wait();
+      return;
+    }
     __threadfence();
     if (tid == 0) a.arrived[item] = 0;
   }
-  for (int row = 0; row < G; ++row) {
-    float M, L, O;
+  pdl_wait();  // the prompt's parts are complete
+  for (int row = warp; row < G; row += kOwnWarps) {
+    Joined r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (active > 1)
-      merge(part, active, (int64_t)G * kPart, row, M, L, O);
+      absorb(r, part + row * kPartRow, active, (int64_t)G * kPartRow);
     else
-      merge(sp, kOwnWarps, (int64_t)G * kPart, row, M, L, O);
+      absorb(r, sp + row * kPartRow, kOwnWarps, (int64_t)G * kPartRow);
+    const int64_t rows = (int64_t)a.B * G;
+    absorb(r, a.pre_part + ((int64_t)g * a.pre_splits * rows + (int64_t)b * G + row) * kPartRow, a.pre_splits, rows * kPartRow);
     const int h = g * G + row;
-    // L is 0 where no key has a weight; a NaN score makes L NaN and goes on to the result
-    static_cast<T*>(a.out)[(int64_t)b * a.out_stride + h * D + tid] = round_to<T>(L == 0.f ? 0.f : O / L);
-    if (a.lse && tid == 0)
-      a.lse[(int64_t)b * a.Hkv * G + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    // l is 0 where no key has a weight; a NaN score makes l NaN and goes on to the result
+    const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+    T* dst = static_cast<T*>(a.out) + (int64_t)b * a.out_stride + h * D + lane * 4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_pair<T>(r.o.x * inv, r.o.y * inv), pack_pair<T>(r.o.z * inv, r.o.w * inv));
+    if (a.lse && lane == 0)
+      a.lse[(int64_t)b * a.Hkv * G + h] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
   }
 }
 
@@ -380,27 +399,32 @@ int own_splits(int B, int Hkv, int64_t keys) {
 }
 
 struct Plan {
-  int splits;
-  size_t part, arrived, total;
+  int splits, pre_splits, pre_per;
+  size_t part, pre_part, total;  // byte offsets in the workspace; the arrival counters come first
 };
 Plan plan_of(int B, int Hkv, int G, int P, int64_t max_own) {
-  Plan p;
-  p.splits = own_splits(B, Hkv, P + max_own);
-  p.arrived = 0;
+  Plan p = {};
+  // One sequence shares nothing, and a prompt of a few chunks costs less to read again than a
+  // second kernel: there the prompt's keys are the first chunks of every sequence.
+  const bool shared = B > 1 && P >= kMinShared;
+  if (shared) prefix_tc_split(B * G, Hkv, P, &p.pre_splits, &p.pre_per);
+  p.splits = own_splits(B, Hkv, max_own + (shared ? 0 : P));
+  const size_t row = kPartRow * sizeof(float);
   p.part = ((size_t)B * Hkv * 4 + 255) / 256 * 256;
-  p.total = p.part + (p.splits > 1 ? (size_t)B * Hkv * p.splits * G * kPart * 4 : 0);
+  p.pre_part = p.part + (p.splits > 1 ? (size_t)B * Hkv * p.splits * G * row : 0);
+  p.total = p.pre_part + (size_t)p.pre_splits * B * Hkv * G * row;
   return p;
 }
 
 template <typename T>
 cudaError_t launch_own(const SharedAttnArgs& a, cudaStream_t s) {
   const size_t smem = std::max<size_t>(kOwnWarps * kOwnStages * kStageBytes,
-                                       (size_t)kOwnWarps * a.G * kPart * 4);
+                                       (size_t)kOwnWarps * a.G * kPartRow * 4);
   cudaError_t e = cudaFuncSetAttribute(own_attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
-  own_attn_kernel<T><<<dim3(a.splits, a.Hkv, a.B), kOwnThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch(own_attn_kernel<T>, dim3(a.splits, a.Hkv, a.B), dim3(kOwnThreads), smem, s,
+                a.pre_splits > 0, a);
 }
 
 bool sizes_ok(int B, int Hq, int Hkv, int D_, int P) {
@@ -443,7 +467,9 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
     VV_CHECK_ARG(k_prefix && v_prefix, "vv_gqa_prefix_attn: prefix_len %d without a prefix",
                  prefix_len);
     VV_CHECK_SHAPE(prefix_token_stride >= D_ && prefix_token_stride % 8 == 0 &&
-                       prefix_head_stride >= 0 && prefix_head_stride % 8 == 0,
+                       (Hkv == 1 || prefix_head_stride >= D_) && prefix_head_stride % 8 == 0 &&
+                       prefix_token_stride < (int64_t(1) << 38) &&
+                       prefix_head_stride < (int64_t(1) << 38),
                    "vv_gqa_prefix_attn: prefix strides %lld, %lld (multiples of 8 elements)",
                    (long long)prefix_head_stride, (long long)prefix_token_stride);
   }
@@ -463,8 +489,10 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
   a.lens = own_lens;
   a.out = out;
   a.lse = lse;
-  a.arrived = reinterpret_cast<unsigned*>(static_cast<char*>(ws) + p.arrived);
+  a.arrived = static_cast<unsigned*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
+  a.pre_part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.pre_part);
+  a.pre_splits = p.pre_splits;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.pre_head = prefix_head_stride;
@@ -482,6 +510,25 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
   a.splits = p.splits;
   a.c = scale * vv::kLog2e;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.pre_splits) {
+    vv::PrefixTcArgs t = {};
+    t.q = q;
+    t.k = k_prefix;
+    t.v = v_prefix;
+    t.part = const_cast<float*>(a.pre_part);
+    t.q_stride = q_stride;
+    t.head = prefix_head_stride;
+    t.token = prefix_token_stride;
+    t.B = B;
+    t.Hkv = Hkv;
+    t.G = G;
+    t.P = prefix_len;
+    t.splits = p.pre_splits;
+    t.per = p.pre_per;
+    t.c = a.c;
+    t.dtype = kv->dtype;
+    VV_CUDA(vv::launch_prefix_tc(t, s));
+  }
   const cudaError_t e = kv->dtype == VV_F16 ? vv::launch_own<__half>(a, s) : vv::launch_own<__nv_bfloat16>(a, s);
   return vv::cuda_check(e, "vv_gqa_prefix_attn launch");
 }

@@ -1,0 +1,392 @@
+// The shared prompt's part of vv_gqa_prefix_attn: all sequences' queries against the same keys,
+// each key read once per 128 query rows.
+//
+//   S = scale Q K^T,  P = 2^(S log2e - m),  o = P V,  l = sum P     per row of Q
+//
+// The rows of one key-value head (sequence x query head of the group) fill the 128 lanes of
+// tensor memory: 64 sequences of 7 heads are 3.5 tiles, where one sequence alone would fill 5% of
+// one.  One CTA = one tile of 128 rows, one key-value head, one part of the keys, on the
+// 5th-generation tensor cores:
+//   warp 0      : copies of the K tiles (128 keys, 128-byte swizzle) into a three-stage ring, a
+//                 stage free again once the S product that read it is done;
+//   warp 2      : the V tiles into a two-stage ring;
+//   warp 1      : tensor memory (2 x S / P, 2 x O: 512 columns) and, one thread, the products
+//                 S_j = Q K_j^T and O_{j % 2} += P_j V_j (P_j from tensor memory, V read
+//                 MN-major straight from the row-major tile);
+//   warps 4..7, 8..11: softmax of the even and of the odd blocks, one thread per row.
+// Even and odd key blocks are two independent softmax streams with a maximum, sum and O of their
+// own: while one stream's exponentials run, the tensor pipe works for the other, and no row needs
+// a second thread (no exchange of maxima).  The streams are joined at the end through shared
+// memory and the tile's partial rows (o, m, l) go to the workspace in fp32; the caller's second
+// kernel joins the parts.  O is rescaled only when a block's maximum exceeds the running one by
+// more than 2^8: weights stay below 2^8, and the same reference divides them out.
+// The weights are rounded to the element type because the tensor cores multiply 16-bit operands;
+// their sum l is taken before that rounding.
+// Every mbarrier wait is bounded; tensor memory is released before the CTA exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "attn_shared.h"
+#include "attn_tc.cuh"
+#include "vv_device.cuh"
+#include "vv_internal.h"
+
+namespace vv {
+namespace {
+
+using namespace tc;
+
+constexpr int D = 128;
+constexpr int BM = 128;   // query rows per CTA
+constexpr int BN = 128;   // keys per block
+constexpr int kThreads = 384;
+constexpr int kKStages = 3, kVStages = 2;
+constexpr int kTiles = 1 + kKStages + kVStages;
+constexpr float kRescale = 8.0f;
+constexpr uint32_t kBarBytes = 256;
+constexpr int kJoinRow = 132;  // floats per row of the join buffer (conflict-free float4 columns)
+constexpr size_t kSmem = kTiles * kTile + kBarBytes + 2 * BM * 8 + 1024;
+static_assert(BM * kJoinRow * 4 <= (kKStages + kVStages) * kTile, "the join buffer lies over the rings");
+
+// instruction descriptor (kind::f16, D f32, M = N = 128): A and B fp16 (0) or bf16 (1)
+template <typename T>
+constexpr uint32_t idesc(bool b_mn) {
+  const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(BN >> 3) << 17) |
+         ((uint32_t)(BM >> 4) << 24);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack_w(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack_w<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack_w<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+struct KvMaps {
+  CUtensorMap k, v;  // dims {D, P, Hkv}, box {64, 128, 1}; rows past P read as zeros
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ KvMaps mp, const __grid_constant__ PrefixTcArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* sQ = smem;
+  unsigned char* sK = smem + kTile;
+  unsigned char* sV = smem + (1 + kKStages) * kTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kTiles * kTile);
+  uint64_t* k_full = bars;                  // [kKStages]
+  uint64_t* k_empty = k_full + kKStages;    // [kKStages]
+  uint64_t* v_full = k_empty + kKStages;    // [kVStages]
+  uint64_t* v_empty = v_full + kVStages;    // [kVStages]
+  uint64_t* s_full = v_empty + kVStages;    // [2]
+  uint64_t* p_full = s_full + 2;            // [2]
+  uint64_t* pv_done = p_full + 2;           // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 2);
+  float2(*ml)[BM] = reinterpret_cast<float2(*)[BM]>(smem + kTiles * kTile + kBarBytes);  // [2][BM]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rows = a.B * a.G;
+  const int r0 = blockIdx.x * BM, split = blockIdx.y, g = blockIdx.z;
+  const int blocks = (a.P + BN - 1) / BN;
+  const int j0 = split * a.per, n = min(a.per, blocks - j0);  // n >= 1 by the launch's grid
+
+  // the second kernel's own work (the sequences' pages) needs nothing of this one
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // Q: two threads per row, 64 dimensions each, into the swizzled K-major atoms; rows past the
+  // last are zero
+  if (tid >= 128) {
+    const int r = (tid - 128) >> 1, half = tid & 1, row = r0 + r;
+    const T* src = nullptr;
+    if (row < rows) {
+      const int b = row / a.G, h = row - b * a.G;
+      src = static_cast<const T*>(a.q) + (int64_t)b * a.q_stride + (int64_t)(g * a.G + h) * D + half * 64;
+    }
+    unsigned char* dst = sQ + half * kAtom + r * 128;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = src ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(dst + ((i ^ (r & 7)) << 4)) = v;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor core reads it
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tmem_slot;
+  auto tS = [tmem](int s) { return tmem + (uint32_t)(s * 128); };
+  auto tO = [tmem](int s) { return tmem + 256u + (uint32_t)(s * 128); };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int j = 0; j < n; ++j) {
+        const int st = j % kKStages;
+        if (j >= kKStages) mbar_wait(&k_empty[st], (j / kKStages - 1) & 1);
+        unsigned char* kt = sK + st * kTile;
+        mbar_arrive_expect_tx(&k_full[st], kTile);
+        tma_load_3d(kt, &mp.k, 0, (j0 + j) * BN, g, &k_full[st]);
+        tma_load_3d(kt + kAtom, &mp.k, 64, (j0 + j) * BN, g, &k_full[st]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    if (lane == 0) {
+      for (int j = 0; j < n; ++j) {
+        const int st = j % kVStages;
+        if (j >= kVStages) mbar_wait(&v_empty[st], (j / kVStages - 1) & 1);
+        unsigned char* vt = sV + st * kTile;
+        mbar_arrive_expect_tx(&v_full[st], kTile);
+        tma_load_3d(vt, &mp.v, 0, (j0 + j) * BN, g, &v_full[st]);
+        tma_load_3d(vt + kAtom, &mp.v, 64, (j0 + j) * BN, g, &v_full[st]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t qa = smem_u32(sQ);
+      constexpr uint32_t kIdS = idesc<T>(false), kIdPV = idesc<T>(true);
+      auto issue_s = [&](int j) {
+        const int st = j % kKStages, s = j & 1;
+        mbar_wait(&k_full[st], (j / kKStages) & 1);
+        tc_after();
+        const uint32_t kb = smem_u32(sK + st * kTile);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 32;
+          mma_ss(tS(s), desc_k_sw128(qa + off), desc_k_sw128(kb + off), kIdS, k > 0 ? 1u : 0u);
+        }
+        mma_commit(&s_full[s]);
+        mma_commit(&k_empty[st]);
+      };
+      issue_s(0);
+      if (n > 1) issue_s(1);
+      for (int j = 0; j < n; ++j) {
+        const int s = j & 1, vs = j % kVStages;
+        mbar_wait(&p_full[s], (j >> 1) & 1);
+        mbar_wait(&v_full[vs], (j / kVStages) & 1);
+        tc_after();
+        const uint32_t vb = smem_u32(sV + vs * kTile);
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          mma_ts(tO(s), tS(s) + (uint32_t)(k * 8), desc_mn_sw128(vb + (uint32_t)k * 2048), kIdPV,
+                 (j > 1 || k > 0) ? 1u : 0u);
+        mma_commit(&v_empty[vs]);
+        mma_commit(&pv_done[s]);
+        if (j + 2 < n) {
+          // S_{j+2} overwrites P_j: not before P_j V_j has read it
+          mbar_wait(&pv_done[s], (j >> 1) & 1);
+          tc_after();
+          issue_s(j + 2);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int s = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const float c = a.c;
+    float m_used = -INFINITY, l = 0.f;
+    for (int j = s; j < n; j += 2) {
+      const uint32_t par = (j >> 1) & 1;
+      mbar_wait(&s_full[s], par);
+      tc_after();
+      uint32_t sr[4][32];
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS(s) + lane_off + (uint32_t)(cc * 32), sr[cc]);
+      tmem_wait_ld();
+      const int left = a.P - (j0 + j) * BN;  // keys of this block
+      if (left < BN) {
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+#pragma unroll
+          for (int t = 0; t < 32; ++t)
+            if (cc * 32 + t >= left) sr[cc][t] = __float_as_uint(-INFINITY);
+        }
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+#pragma unroll
+        for (int t = 0; t < 32; ++t) m4[t & 3] = fmaxf(m4[t & 3], __uint_as_float(sr[cc][t]));
+      }
+      const float mb = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+      const bool move = mb > m_used + kRescale;
+      const float m_new = move ? mb : m_used;
+      if (j > 1 && __any_sync(0xffffffffu, move)) {
+        const float corr = move ? ex2_approx(m_used - m_new) : 1.f;
+        mbar_wait(&pv_done[s], par ^ 1);  // O holds the blocks before
+        tc_after();
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(tO(s) + lane_off + (uint32_t)(cc * 32), o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * corr);
+          tmem_st32(tO(s) + lane_off + (uint32_t)(cc * 32), o);
+        }
+        l *= corr;
+      }
+      m_used = m_new;
+      const float ref = m_used == -INFINITY ? 0.f : m_used;  // nothing above -inf yet: weights 0
+      float ls0 = 0.f, ls1 = 0.f;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t pp[32];
+#pragma unroll
+        for (int t = 0; t < 64; t += 2) {
+          const float e0 = ex2_approx(fmaf(__uint_as_float(sr[hh * 2 + (t >> 5)][t & 31]), c, -ref));
+          const float e1 = ex2_approx(fmaf(__uint_as_float(sr[hh * 2 + (t >> 5)][(t & 31) + 1]), c, -ref));
+          ls0 += e0;
+          ls1 += e1;
+          pp[t >> 1] = pack_w<T>(e0, e1);
+        }
+        tmem_st32(tS(s) + lane_off + (uint32_t)(hh * 32), pp);
+      }
+      l += ls0 + ls1;
+      tmem_wait_st();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[s]);
+    }
+    // ---- join the two streams: stream 0 keeps dimensions 0..63, stream 1 64..127; each hands the
+    // other half of its scaled O over through shared memory (the rings are idle by then)
+    ml[s][r] = make_float2(m_used, l);
+    if (n > s) mbar_wait(&pv_done[s], ((n - 1 - s) / 2) & 1);  // this stream's last product
+    tc_after();
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float2 other = ml[s ^ 1][r];
+    const float M = fmaxf(m_used, other.x), ref = M == -INFINITY ? 0.f : M;
+    const float w = ex2_approx(m_used - ref), wo = ex2_approx(other.x - ref);
+    const bool have = n > s;
+    float* join = reinterpret_cast<float*>(sK);
+    auto scaled = [&](int cc, float (&o)[32]) {  // 32 columns of this stream's O times w
+      uint32_t t32[32];
+      if (have) {
+        tmem_ld32(tO(s) + lane_off + (uint32_t)(cc * 32), t32);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int t = 0; t < 32; ++t) o[t] = have ? __uint_as_float(t32[t]) * w : 0.f;
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int cc = (s ^ 1) * 2 + i;
+      float o[32];
+      scaled(cc, o);
+#pragma unroll
+      for (int t = 0; t < 32; t += 4)
+        *reinterpret_cast<float4*>(join + r * kJoinRow + cc * 32 + t) = make_float4(o[t], o[t + 1], o[t + 2], o[t + 3]);
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const int row = r0 + r;
+    float* dst = a.part + (((int64_t)g * a.splits + split) * rows + row) * kPartRow;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int cc = s * 2 + i;
+      float o[32];
+      scaled(cc, o);
+      if (row < rows) {
+#pragma unroll
+        for (int t = 0; t < 32; t += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(join + r * kJoinRow + cc * 32 + t);
+          *reinterpret_cast<float4*>(dst + cc * 32 + t) = make_float4(o[t] + x.x, o[t + 1] + x.y, o[t + 2] + x.z, o[t + 3] + x.w);
+        }
+      }
+    }
+    if (s == 0 && row < rows) *reinterpret_cast<float2*>(dst + D) = make_float2(M, l * w + other.y * wo);
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <typename T>
+cudaError_t launch_t(const KvMaps& mp, const PrefixTcArgs& a, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((a.B * a.G + BM - 1) / BM, a.splits, a.Hkv);
+  prefix_tc_kernel<T><<<grid, kThreads, kSmem, s>>>(mp, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+void prefix_tc_split(int rows, int Hkv, int P, int* splits, int* per) {
+  // as many parts as fill one wave of the SMs, of equally many 128-key blocks; with more tiles
+  // than SMs, the number of parts (up to 8) whose last wave wastes least, at about two blocks'
+  // time for a part's start and end
+  const int64_t tiles = (int64_t)((rows + BM - 1) / BM) * Hkv, sms = sm_count();
+  const int blocks = (P + BN - 1) / BN;
+  int64_t best = INT64_MAX;
+  const int most = (int)std::min<int64_t>(blocks, std::max<int64_t>(8, sms / tiles));
+  for (int s = 1; s <= most; ++s) {
+    const int p = (blocks + s - 1) / s, used = (blocks + p - 1) / p;
+    const int64_t cost = (tiles * used + sms - 1) / sms * (p + 2);
+    if (cost < best) {
+      best = cost;
+      *splits = used;
+      *per = p;
+    }
+  }
+}
+
+cudaError_t launch_prefix_tc(const PrefixTcArgs& a, cudaStream_t s) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  KvMaps mp;
+  for (int t = 0; t < 2; ++t) {
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.P, (cuuint64_t)a.Hkv};
+    cuuint64_t strides[2] = {(cuuint64_t)a.token * 2,
+                             (cuuint64_t)(a.Hkv > 1 ? a.head : a.token) * 2};
+    cuuint32_t box[3] = {64, BN, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    if (fn(t == 0 ? &mp.k : &mp.v,
+           a.dtype == VV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+           3, const_cast<void*>(t == 0 ? a.k : a.v), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  return a.dtype == VV_F16 ? launch_t<__half>(mp, a, s) : launch_t<__nv_bfloat16>(mp, a, s);
+}
+
+}  // namespace vv
