@@ -10,18 +10,23 @@
 //   warp 0      : copies of the K tiles (128 keys, 128-byte swizzle) into a three-stage ring, a
 //                 stage free again once the S product that read it is done;
 //   warp 2      : the V tiles into a two-stage ring;
-//   warp 1      : tensor memory (2 x S / P, 2 x O: 512 columns) and, one thread, the products
-//                 S_j = Q K_j^T and O_{j % 2} += P_j V_j (P_j from tensor memory, V read
-//                 MN-major straight from the row-major tile);
+//   warp 1      : tensor memory (2 x S, 2 x P, O: 512 columns) and the products S_j = Q K_j^T;
+//   warp 3      : the products O += P_j V_j (P_j from tensor memory, V read MN-major straight from
+//                 the row-major tile); waits and commits of one kind of product then pass while the
+//                 other kind keeps the tensor core busy;
 //   warps 4..7, 8..11: softmax of the even and of the odd blocks, one thread per row.
-// Even and odd key blocks are two independent softmax streams with a maximum, sum and O of their
-// own: while one stream's exponentials run, the tensor pipe works for the other, and no row needs
-// a second thread (no exchange of maxima).  The streams are joined at the end through shared
-// memory and the tile's partial rows (o, m, l) go to the workspace in fp32; the caller's second
-// kernel joins the parts.  O is rescaled only when a block's maximum exceeds the running one by
-// more than 2^8: weights stay below 2^8, and the same reference divides them out.
+// A thread takes its row's 128 scores of a block into registers, which frees the S buffer at once:
+// S_{j+2} is queued ahead of P_j V_j, so the tensor core never waits for exponentials that it does
+// not need, and a group's next scores are there when it has stored its weights.  A maximum needs
+// no exchange inside a block; the two groups hand the row's running maximum on from block to block
+// through shared memory (a one-way named barrier per 32 rows), so that one O serves both.  While
+// one group's exponentials run (128 a row and block: 1024 cycles of the special-function units)
+// the other loads, finds its maximum and stores.  O is rescaled only when a block's maximum
+// exceeds the running one by more than 2^8: weights stay below 2^8, and the same reference divides
+// them out.
 // The weights are rounded to the element type because the tensor cores multiply 16-bit operands;
-// their sum l is taken before that rounding.
+// their sum l is taken before that rounding.  The tile's partial rows (o, m, l) go to the workspace
+// in fp32; the caller's second kernel joins the parts.
 // Every mbarrier wait is bounded; tensor memory is released before the CTA exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -44,13 +49,13 @@ constexpr int D = 128;
 constexpr int BM = 128;   // query rows per CTA
 constexpr int BN = 128;   // keys per block
 constexpr int kThreads = 384;
-constexpr int kKStages = 3, kVStages = 2;
+constexpr int kKStages = 3, kVStages = 2;  // V_j, P_j and S_j share the index j & 1
 constexpr int kTiles = 1 + kKStages + kVStages;
 constexpr float kRescale = 8.0f;
 constexpr uint32_t kBarBytes = 256;
-constexpr int kJoinRow = 132;  // floats per row of the join buffer (conflict-free float4 columns)
-constexpr size_t kSmem = kTiles * kTile + kBarBytes + 2 * BM * 8 + 1024;
-static_assert(BM * kJoinRow * 4 <= (kKStages + kVStages) * kTile, "the join buffer lies over the rings");
+constexpr int kOutRow = 132;  // floats per row of the output stage (conflict-free float4 columns)
+constexpr size_t kSmem = kTiles * kTile + kBarBytes + 2 * BM * 4 + 2 * BM * 8 + 1024;
+static_assert(BM * kOutRow * 4 <= (kKStages + kVStages) * kTile, "the output stage lies over the rings");
 
 // instruction descriptor (kind::f16, D f32, M = N = 128): A and B fp16 (0) or bf16 (1)
 template <typename T>
@@ -73,6 +78,15 @@ __device__ __forceinline__ uint32_t pack_w<__nv_bfloat16>(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A wait of this kernel is some hundred cycles; the bounded wait reads the global timer first, which
+// costs more than that.  So a few plain tries (each sleeps in hardware for a while) come first.
+__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return;
+  mbar_wait(bar, parity);
+}
+
 struct KvMaps {
   CUtensorMap k, v;  // dims {D, P, Hkv}, box {64, 128, 1}; rows past P read as zeros
 };
@@ -90,12 +104,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_full = bars;                  // [kKStages]
   uint64_t* k_empty = k_full + kKStages;    // [kKStages]
   uint64_t* v_full = k_empty + kKStages;    // [kVStages]
-  uint64_t* v_empty = v_full + kVStages;    // [kVStages]
-  uint64_t* s_full = v_empty + kVStages;    // [2]
-  uint64_t* p_full = s_full + 2;            // [2]
-  uint64_t* pv_done = p_full + 2;           // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 2);
-  float2(*ml)[BM] = reinterpret_cast<float2(*)[BM]>(smem + kTiles * kTile + kBarBytes);  // [2][BM]
+  uint64_t* s_full = v_full + kVStages;     // [2]
+  uint64_t* s_free = s_full + 2;            // [2] scores are in registers
+  uint64_t* p_full = s_free + 2;            // [2]
+  uint64_t* pv_done = p_full + 2;           // [2] also frees the V stage
+  uint64_t* o_done = pv_done + 2;           // all products: one phase, waited for by both groups
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 1);
+  float(*m_row)[BM] = reinterpret_cast<float(*)[BM]>(smem + kTiles * kTile + kBarBytes);  // [2][BM]
+  float2(*ml)[BM] = reinterpret_cast<float2(*)[BM]>(smem + kTiles * kTile + kBarBytes + 2 * BM * 4);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rows = a.B * a.G;
@@ -105,21 +121,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the second kernel's own work (the sequences' pages) needs nothing of this one
   pdl_launch_dependents();
+  auto load_k = [&](int j) {
+    const int st = j % kKStages;
+    unsigned char* kt = sK + st * kTile;
+    mbar_arrive_expect_tx(&k_full[st], kTile);
+    tma_load_3d(kt, &mp.k, 0, (j0 + j) * BN, g, &k_full[st]);
+    tma_load_3d(kt + kAtom, &mp.k, 64, (j0 + j) * BN, g, &k_full[st]);
+  };
+  auto load_v = [&](int j) {
+    const int st = j % kVStages;
+    unsigned char* vt = sV + st * kTile;
+    mbar_arrive_expect_tx(&v_full[st], kTile);
+    tma_load_3d(vt, &mp.v, 0, (j0 + j) * BN, g, &v_full[st]);
+    tma_load_3d(vt + kAtom, &mp.v, 64, (j0 + j) * BN, g, &v_full[st]);
+  };
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
     }
-    for (int i = 0; i < kVStages; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
+    for (int i = 0; i < kVStages; ++i) mbar_init(&v_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
+    mbar_init(o_done, 1);
     fence_mbar_init();
+    // the rings' first fill is on its way before the rest of the CTA is ready
+    for (int j = 0; j < min(n, kKStages); ++j) load_k(j);
+    for (int j = 0; j < min(n, kVStages); ++j) load_v(j);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -131,103 +163,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   // last are zero
   if (tid >= 128) {
     const int r = (tid - 128) >> 1, half = tid & 1, row = r0 + r;
-    const T* src = nullptr;
+    uint4 v[8];
     if (row < rows) {
       const int b = row / a.G, h = row - b * a.G;
-      src = static_cast<const T*>(a.q) + (int64_t)b * a.q_stride + (int64_t)(g * a.G + h) * D + half * 64;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const T*>(a.q) + (int64_t)b * a.q_stride + (int64_t)(g * a.G + h) * D + half * 64);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = src[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
     }
     unsigned char* dst = sQ + half * kAtom + r * 128;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 v = src ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(dst + ((i ^ (r & 7)) << 4)) = v;
-    }
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + ((i ^ (r & 7)) << 4)) = v[i];
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor core reads it
   }
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = *tmem_slot;
-  auto tS = [tmem](int s) { return tmem + (uint32_t)(s * 128); };
-  auto tO = [tmem](int s) { return tmem + 256u + (uint32_t)(s * 128); };
+  auto tS = [tmem](int i) { return tmem + (uint32_t)(i * 128); };
+  auto tP = [tmem](int i) { return tmem + 256u + (uint32_t)(i * 64); };
+  const uint32_t tO = tmem + 384u;
 
   if (warp == 0) {
     if (lane == 0) {
-      for (int j = 0; j < n; ++j) {
-        const int st = j % kKStages;
-        if (j >= kKStages) mbar_wait(&k_empty[st], (j / kKStages - 1) & 1);
-        unsigned char* kt = sK + st * kTile;
-        mbar_arrive_expect_tx(&k_full[st], kTile);
-        tma_load_3d(kt, &mp.k, 0, (j0 + j) * BN, g, &k_full[st]);
-        tma_load_3d(kt + kAtom, &mp.k, 64, (j0 + j) * BN, g, &k_full[st]);
+      for (int j = kKStages; j < n; ++j) {
+        wait_phase(&k_empty[j % kKStages], (j / kKStages - 1) & 1);
+        load_k(j);
       }
     }
     __syncwarp();
   } else if (warp == 2) {
     if (lane == 0) {
-      for (int j = 0; j < n; ++j) {
-        const int st = j % kVStages;
-        if (j >= kVStages) mbar_wait(&v_empty[st], (j / kVStages - 1) & 1);
-        unsigned char* vt = sV + st * kTile;
-        mbar_arrive_expect_tx(&v_full[st], kTile);
-        tma_load_3d(vt, &mp.v, 0, (j0 + j) * BN, g, &v_full[st]);
-        tma_load_3d(vt + kAtom, &mp.v, 64, (j0 + j) * BN, g, &v_full[st]);
+      for (int j = kVStages; j < n; ++j) {
+        wait_phase(&pv_done[j & 1], ((j >> 1) - 1) & 1);
+        load_v(j);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t qa = smem_u32(sQ);
-      constexpr uint32_t kIdS = idesc<T>(false), kIdPV = idesc<T>(true);
-      auto issue_s = [&](int j) {
-        const int st = j % kKStages, s = j & 1;
-        mbar_wait(&k_full[st], (j / kKStages) & 1);
-        tc_after();
-        const uint32_t kb = smem_u32(sK + st * kTile);
+    const uint32_t qa = smem_u32(sQ);
+    constexpr uint32_t kIdS = idesc<T>(false);
+    auto issue_s = [&](int j) {
+      const int st = j % kKStages, sb = j & 1;
+      wait_phase(&k_full[st], (j / kKStages) & 1);
+      tc_after();
+      const uint32_t kb = smem_u32(sK + st * kTile);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 32;
-          mma_ss(tS(s), desc_k_sw128(qa + off), desc_k_sw128(kb + off), kIdS, k > 0 ? 1u : 0u);
-        }
-        mma_commit(&s_full[s]);
-        mma_commit(&k_empty[st]);
-      };
-      issue_s(0);
-      if (n > 1) issue_s(1);
-      for (int j = 0; j < n; ++j) {
-        const int s = j & 1, vs = j % kVStages;
-        mbar_wait(&p_full[s], (j >> 1) & 1);
-        mbar_wait(&v_full[vs], (j / kVStages) & 1);
-        tc_after();
-        const uint32_t vb = smem_u32(sV + vs * kTile);
-#pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          mma_ts(tO(s), tS(s) + (uint32_t)(k * 8), desc_mn_sw128(vb + (uint32_t)k * 2048), kIdPV,
-                 (j > 1 || k > 0) ? 1u : 0u);
-        mma_commit(&v_empty[vs]);
-        mma_commit(&pv_done[s]);
-        if (j + 2 < n) {
-          // S_{j+2} overwrites P_j: not before P_j V_j has read it
-          mbar_wait(&pv_done[s], (j >> 1) & 1);
-          tc_after();
-          issue_s(j + 2);
-        }
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 32;
+        mma_ss_elect(tS(sb), desc_k_sw128(qa + off), desc_k_sw128(kb + off), kIdS, k > 0 ? 1u : 0u);
       }
+      mma_commit_elect(&s_full[sb]);
+      mma_commit_elect(&k_empty[st]);
+    };
+    issue_s(0);
+    if (n > 1) issue_s(1);
+    for (int j = 2; j < n; ++j) {
+      wait_phase(&s_free[j & 1], ((j >> 1) - 1) & 1);
+      issue_s(j);
     }
-    __syncwarp();
+  } else if (warp == 3) {
+    constexpr uint32_t kIdPV = idesc<T>(true);
+    for (int j = 0; j < n; ++j) {
+      const int sb = j & 1;
+      wait_phase(&v_full[sb], (j >> 1) & 1);
+      wait_phase(&p_full[sb], (j >> 1) & 1);
+      tc_after();
+      const uint32_t vb = smem_u32(sV + sb * kTile);
+#pragma unroll
+      for (int k = 0; k < BN / 16; ++k)
+        mma_ts_elect(tO, tP(sb) + (uint32_t)(k * 8), desc_mn_sw128(vb + (uint32_t)k * 2048), kIdPV,
+                     (j > 0 || k > 0) ? 1u : 0u);
+      mma_commit_elect(&pv_done[sb]);
+    }
+    mma_commit_elect(o_done);
   } else if (warp >= 4) {
     const int s = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const float c = a.c;
-    float m_used = -INFINITY, l = 0.f;
+    float m_mine = -INFINITY, l = 0.f;  // l: this group's blocks, relative to m_mine
     for (int j = s; j < n; j += 2) {
-      const uint32_t par = (j >> 1) & 1;
-      mbar_wait(&s_full[s], par);
+      wait_phase(&s_full[s], (j >> 1) & 1);
       tc_after();
       uint32_t sr[4][32];
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS(s) + lane_off + (uint32_t)(cc * 32), sr[cc]);
       tmem_wait_ld();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[s]);
       const int left = a.P - (j0 + j) * BN;  // keys of this block
       if (left < BN) {
 #pragma unroll
@@ -244,25 +271,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 32; ++t) m4[t & 3] = fmaxf(m4[t & 3], __uint_as_float(sr[cc][t]));
       }
       const float mb = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-      const bool move = mb > m_used + kRescale;
-      const float m_new = move ? mb : m_used;
-      if (j > 1 && __any_sync(0xffffffffu, move)) {
-        const float corr = move ? ex2_approx(m_used - m_new) : 1.f;
-        mbar_wait(&pv_done[s], par ^ 1);  // O holds the blocks before
+      // the running reference after block j - 1, from the other group's warp of the same rows
+      float m_prev = -INFINITY;
+      if (j > 0) {
+        asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter * 2 + (s ^ 1)) : "memory");
+        m_prev = m_row[s ^ 1][r];
+      }
+      const bool move = mb > m_prev + kRescale;
+      const float m_new = move ? mb : m_prev;
+      if (j + 1 < n) {
+        m_row[s][r] = m_new;
+        asm volatile("bar.arrive %0, 64;" ::"r"(2 + quarter * 2 + s) : "memory");
+      }
+      if (j > 0 && __any_sync(0xffffffffu, move)) {
+        const float corr = move ? ex2_approx(m_prev - m_new) : 1.f;
+        wait_phase(&pv_done[s ^ 1], ((j - 1) >> 1) & 1);  // O holds the blocks before
         tc_after();
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t o[32];
-          tmem_ld32(tO(s) + lane_off + (uint32_t)(cc * 32), o);
+#pragma unroll 1
+        for (int cc = 0; cc < 8; ++cc) {  // 16 columns at a time: the scores stay in registers
+          uint32_t o[16];
+          tmem_ld16(tO + lane_off + (uint32_t)(cc * 16), o);
           tmem_wait_ld();
 #pragma unroll
-          for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * corr);
-          tmem_st32(tO(s) + lane_off + (uint32_t)(cc * 32), o);
+          for (int t = 0; t < 16; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * corr);
+          tmem_st16(tO + lane_off + (uint32_t)(cc * 16), o);
         }
-        l *= corr;
       }
-      m_used = m_new;
-      const float ref = m_used == -INFINITY ? 0.f : m_used;  // nothing above -inf yet: weights 0
+      const float ref = m_new == -INFINITY ? 0.f : m_new;  // nothing above -inf yet: weights 0
+      l *= ex2_approx(m_mine - ref);
+      m_mine = m_new;
+      if (j > 1) wait_phase(&pv_done[s], ((j >> 1) - 1) & 1);  // P_{j-2} has been read
       float ls0 = 0.f, ls1 = 0.f;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -275,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ls1 += e1;
           pp[t >> 1] = pack_w<T>(e0, e1);
         }
-        tmem_st32(tS(s) + lane_off + (uint32_t)(hh * 32), pp);
+        tmem_st32(tP(s) + lane_off + (uint32_t)(hh * 32), pp);
       }
       l += ls0 + ls1;
       tmem_wait_st();
@@ -283,52 +321,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[s]);
     }
-    // ---- join the two streams: stream 0 keeps dimensions 0..63, stream 1 64..127; each hands the
-    // other half of its scaled O over through shared memory (the rings are idle by then)
-    ml[s][r] = make_float2(m_used, l);
-    if (n > s) mbar_wait(&pv_done[s], ((n - 1 - s) / 2) & 1);  // this stream's last product
+    // ---- the tile's partial rows: o through shared memory (the rings are idle by then) so that a
+    // warp stores whole rows
+    ml[s][r] = make_float2(m_mine, l);
+    wait_phase(o_done, 0);
     tc_after();
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    const float2 other = ml[s ^ 1][r];
-    const float M = fmaxf(m_used, other.x), ref = M == -INFINITY ? 0.f : M;
-    const float w = ex2_approx(m_used - ref), wo = ex2_approx(other.x - ref);
-    const bool have = n > s;
-    float* join = reinterpret_cast<float*>(sK);
-    auto scaled = [&](int cc, float (&o)[32]) {  // 32 columns of this stream's O times w
-      uint32_t t32[32];
-      if (have) {
-        tmem_ld32(tO(s) + lane_off + (uint32_t)(cc * 32), t32);
-        tmem_wait_ld();
-      }
-#pragma unroll
-      for (int t = 0; t < 32; ++t) o[t] = have ? __uint_as_float(t32[t]) * w : 0.f;
-    };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int cc = (s ^ 1) * 2 + i;
-      float o[32];
-      scaled(cc, o);
-#pragma unroll
-      for (int t = 0; t < 32; t += 4)
-        *reinterpret_cast<float4*>(join + r * kJoinRow + cc * 32 + t) = make_float4(o[t], o[t + 1], o[t + 2], o[t + 3]);
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    const int row = r0 + r;
-    float* dst = a.part + (((int64_t)g * a.splits + split) * rows + row) * kPartRow;
+    float* stage = reinterpret_cast<float*>(sK);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int cc = s * 2 + i;
-      float o[32];
-      scaled(cc, o);
-      if (row < rows) {
+      uint32_t o[32];
+      tmem_ld32(tO + lane_off + (uint32_t)(cc * 32), o);
+      tmem_wait_ld();
 #pragma unroll
-        for (int t = 0; t < 32; t += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(join + r * kJoinRow + cc * 32 + t);
-          *reinterpret_cast<float4*>(dst + cc * 32 + t) = make_float4(o[t] + x.x, o[t + 1] + x.y, o[t + 2] + x.z, o[t + 3] + x.w);
-        }
-      }
+      for (int t = 0; t < 32; t += 4)
+        *reinterpret_cast<uint4*>(stage + r * kOutRow + cc * 32 + t) = make_uint4(o[t], o[t + 1], o[t + 2], o[t + 3]);
     }
-    if (s == 0 && row < rows) *reinterpret_cast<float2*>(dst + D) = make_float2(M, l * w + other.y * wo);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    float* dst = a.part + (((int64_t)g * a.splits + split) * rows + r0) * kPartRow;
+    const int mine = (warp - 4) * 16, left = min(16, rows - r0 - mine);
+#pragma unroll 4
+    for (int i = 0; i < left; ++i)
+      *reinterpret_cast<float4*>(dst + (int64_t)(mine + i) * kPartRow + lane * 4) =
+          *reinterpret_cast<const float4*>(stage + (mine + i) * kOutRow + lane * 4);
+    if (s == 0 && r0 + r < rows) {
+      // the reference of the last block is the row's; l of each group relative to it
+      const float2 other = ml[1][r];
+      const float M = (n - 1) & 1 ? other.x : m_mine, ref = M == -INFINITY ? 0.f : M;
+      *reinterpret_cast<float2*>(dst + (int64_t)r * kPartRow + D) =
+          make_float2(M, l * ex2_approx(m_mine - ref) + other.y * ex2_approx(other.x - ref));
+    }
   }
   tc_before();
   __syncthreads();

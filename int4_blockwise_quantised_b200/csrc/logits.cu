@@ -6,11 +6,11 @@
 //   bias:  x <- x + w                        bit 0: x <- -inf
 //
 // One pass over the logits.  A CTA owns a run of kSlice consecutive tokens of one row; it issues
-// the loads of its logits into registers first and, while they are on their way, clears its
-// tables in shared memory (a count and a `seen` byte per token) and reads the row's whole history,
-// keeping what falls into its run.  Equal ids of a warp are counted by one lane (match), so a
-// prompt of thousands of equal ids (an audio span) does not serialise on one counter; the
-// prompt's ids only set a byte, with plain stores.  The greedy token goes through one 64-bit
+// the loads of its logits into registers first and, while they are on their way, reads the row's
+// whole history, keeping what falls into its run: one bit per token in shared memory says whether
+// it occurs, and only the counters of generated tokens are ever touched.  Equal ids of a warp are
+// counted by one lane (match) and a set bit is not set again, so thousands of equal ids (a
+// prompt's audio span) do not serialise on one address.  The greedy token goes through one 64-bit
 // maximum per row: (order-preserving bits of x, inverted token), whose result does not depend on
 // the order of arrival and picks the lowest token on ties; the last CTA of a row writes it and
 // leaves the workspace zero.
@@ -78,9 +78,10 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const __g
   extern __shared__ __align__(16) unsigned char lsm[];
   __shared__ unsigned long long warp_key[kLogitThreads / 32];
   const bool history = a.r.tokens != nullptr, biased = a.r.bias_ids != nullptr;
-  unsigned* count = reinterpret_cast<unsigned*>(lsm);                       // [kSlice]
-  unsigned char* seen = lsm + kSlice * 4;                                   // [kSlice]
-  unsigned* bias = reinterpret_cast<unsigned*>(lsm + (history ? kSlice * 5 : 0));  // [kSlice]
+  unsigned* count = reinterpret_cast<unsigned*>(lsm);                              // [kSlice]
+  unsigned* bias = reinterpret_cast<unsigned*>(lsm + (history ? kSlice * 4 : 0));  // [kSlice]
+  __shared__ unsigned bits[3][kSlice / 32];
+  constexpr int kSeen = 0, kSaid = 1, kBias = 2;
   const int b = blockIdx.y, v0 = blockIdx.x * kSlice, tid = threadIdx.x;
   const int nv = min(kSlice, a.V - v0);
   const T* in = static_cast<const T*>(a.in) + (int64_t)b * a.in_stride + v0;
@@ -101,48 +102,72 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const __g
     }
   }
 
+  // which tokens of the run the history and the biases name: one bit each, so that nothing else has
+  // to be cleared, and a run of logits without any is only masked and copied
   bool bad = false;
-  if (history || biased) {
-    const int clear = ((history ? kSlice * 5 : 0) + (biased ? kSlice * 4 : 0)) / 16;
-    for (int i = tid; i < clear; i += kLogitThreads)
-      reinterpret_cast<uint4*>(lsm)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-  }
+  int plen = 0, len = 0, i0 = 0, i1 = 0;
+  const int32_t* tok = nullptr;
   if (history) {
     const int raw = a.r.token_lens[b], raw_p = a.r.prompt_lens ? a.r.prompt_lens[b] : 0;
-    const int len = min(max(raw, 0), a.r.max_tokens), plen = min(max(raw_p, 0), len);
+    len = min(max(raw, 0), a.r.max_tokens);
+    plen = min(max(raw_p, 0), len);
     bad = raw != len || raw_p < 0 || raw_p > a.r.max_tokens;
-    const int32_t* tok = a.r.tokens + (int64_t)b * a.r.tokens_stride;
+    tok = a.r.tokens + (int64_t)b * a.r.tokens_stride;
+  }
+  if (biased) {
+    const int raw0 = a.r.bias_offsets[b], raw1 = a.r.bias_offsets[b + 1];
+    i0 = min(max(raw0, 0), a.r.n_bias);
+    i1 = min(max(raw1, i0), a.r.n_bias);
+    bad = bad || raw0 != i0 || raw1 != i1;
+  }
+  if (bad && tid == 0 && blockIdx.x == 0) set_device_error(VV_ERR_RANGE);
+  if (history || biased) {
+    for (int i = tid; i < 3 * kSlice / 32; i += kLogitThreads) (&bits[0][0])[i] = 0;
+    __syncthreads();
+    // a prompt may hold one id thousands of times: the bit is looked at before it is set
+    auto mark = [&](int which, unsigned d) {
+      volatile unsigned* word = &bits[which][d >> 5];
+      if (!((*word >> (d & 31)) & 1)) atomicOr(&bits[which][d >> 5], 1u << (d & 31));
+    };
+#pragma unroll 4
     for (int i = tid; i < plen; i += kLogitThreads) {
       const unsigned d = (unsigned)tok[i] - (unsigned)v0;
-      if (d < (unsigned)nv) seen[d] = 1;
+      if (d < (unsigned)nv) mark(kSeen, d);
     }
-    for (int i0 = plen; i0 < len; i0 += kLogitThreads) {  // whole warps, for the match
-      const int i = i0 + tid;
+#pragma unroll 2
+    for (int i = plen + tid; i < len; i += kLogitThreads) {
+      const unsigned d = (unsigned)tok[i] - (unsigned)v0;
+      if (d < (unsigned)nv) {
+        mark(kSaid, d);
+        count[d] = 0;
+      }
+    }
+    for (int i = i0 + tid; i < i1; i += kLogitThreads) {
+      const unsigned d = (unsigned)a.r.bias_ids[i] - (unsigned)v0;
+      if (d < (unsigned)nv) {
+        mark(kBias, d);
+        bias[d] = 0;
+      }
+    }
+    __syncthreads();
+    for (int j0 = plen; j0 < len; j0 += kLogitThreads) {  // whole warps, for the match
+      const int i = j0 + tid;
       unsigned d = i < len ? (unsigned)tok[i] - (unsigned)v0 : 0xffffffffu;
       if (d >= (unsigned)nv) d = 0xffffffffu;
       const unsigned same = __match_any_sync(0xffffffffu, d);
       if (d != 0xffffffffu && (tid & 31) == __ffs(same) - 1) atomicAdd(&count[d], __popc(same));
     }
-  }
-  if (biased) {
-    // an id named twice keeps its last value: the entry of the largest index wins, then its
-    // value replaces the index
-    const int raw0 = a.r.bias_offsets[b], raw1 = a.r.bias_offsets[b + 1];
-    const int i0 = min(max(raw0, 0), a.r.n_bias), i1 = min(max(raw1, i0), a.r.n_bias);
-    bad = bad || raw0 != i0 || raw1 != i1;
+    // an id named twice keeps its last value: the entry of the largest index wins
     for (int i = i0 + tid; i < i1; i += kLogitThreads) {
       const unsigned d = (unsigned)a.r.bias_ids[i] - (unsigned)v0;
-      if (d < (unsigned)nv) atomicMax(&bias[d], (unsigned)(i - i0 + 1));
+      if (d < (unsigned)nv) atomicMax(&bias[d], (unsigned)i);
     }
+    __syncthreads();
   }
-  if (history || biased) __syncthreads();
-  if (bad && tid == 0 && blockIdx.x == 0) set_device_error(VV_ERR_RANGE);
 
   const float rep = history && a.r.repetition ? a.r.repetition[b] : 1.f;
   const float freq = history && a.r.frequency ? a.r.frequency[b] : 0.f;
   const float pres = history && a.r.presence ? a.r.presence[b] : 0.f;
-  const float* bias_vals = biased ? a.r.bias_vals + max(a.r.bias_offsets[b], 0) - 1 : nullptr;
   const uint32_t* mask = a.r.mask ? a.r.mask + (int64_t)b * a.r.mask_stride : nullptr;
   unsigned long long best = 0;
 #pragma unroll
@@ -150,22 +175,25 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const __g
     const int e0 = (j * kLogitThreads + tid) * VEC;
     if (e0 >= nv) continue;
     // e0 is a multiple of VEC (4 or 8): its bits lie in one word
-    const unsigned bits = mask ? mask[(v0 + e0) >> 5] >> ((v0 + e0) & 31) : 0xffffffffu;
+    const unsigned allowed = mask ? mask[(v0 + e0) >> 5] >> ((v0 + e0) & 31) : 0xffffffffu;
+    unsigned seen = 0, said = 0, named = 0;
+    if (history || biased) {
+      seen = bits[kSeen][e0 >> 5] >> (e0 & 31);
+      said = bits[kSaid][e0 >> 5] >> (e0 & 31);
+      named = bits[kBias][e0 >> 5] >> (e0 & 31);
+    }
+    const bool any = ((seen | said | named) & ((1u << VEC) - 1)) != 0;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const int i = e0 + e;
       if (i >= nv) break;
       float y = to_f32<T>(x[j * VEC + e]);
-      if (history) {
-        const unsigned n = count[i];
-        if (n || seen[i]) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
-        if (n) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)n)), pres);
+      if (any) {
+        if (((seen | said) >> e) & 1) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+        if ((said >> e) & 1) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)count[i])), pres);
+        if ((named >> e) & 1) y = __fadd_rn(y, a.r.bias_vals[bias[i]]);
       }
-      if (biased) {
-        const unsigned k = bias[i];
-        if (k) y = __fadd_rn(y, bias_vals[k]);
-      }
-      if (!((bits >> e) & 1)) y = -INFINITY;
+      if (!((allowed >> e) & 1)) y = -INFINITY;
       x[j * VEC + e] = from_f32<T>(y);
       if (y > -INFINITY) {
         const unsigned long long key = ((unsigned long long)ordered_bits(y) << 32) | (0xffffffffu - (unsigned)(v0 + i));
@@ -205,9 +233,9 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const __g
 
 template <typename T>
 cudaError_t launch_logits(const LogitsArgs& a, int B, cudaStream_t s) {
-  const size_t smem = (a.r.tokens ? kSlice * 5 : 0) + (a.r.bias_ids ? kSlice * 4 : 0);
+  const size_t smem = (a.r.tokens ? kSlice * 4 : 0) + (a.r.bias_ids ? kSlice * 4 : 0);
   cudaError_t e = cudaFuncSetAttribute(logits_process_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSlice * 9);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSlice * 8);
   if (e != cudaSuccess) return e;
   logits_process_kernel<T><<<dim3((a.V + kSlice - 1) / kSlice, B), kLogitThreads, smem, s>>>(a);
   return cudaGetLastError();

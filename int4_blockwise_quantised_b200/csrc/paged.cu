@@ -30,7 +30,7 @@ namespace {
 // a token or page finds its request by bisection in those sums.  A step of a small batch is one
 // CTA: what it costs is the latency of load, scan, bisection and store, not bytes.
 constexpr int kPlanThreads = 512;
-constexpr int kPlanMaxB = 16384;  // two int32 sums per request in shared memory
+constexpr int kPlanMaxB = 16384;  // three int32 per request in shared memory (192 KB)
 
 struct PlanArgs {
   const int32_t* lens;
@@ -46,25 +46,10 @@ struct PlanArgs {
   int B, prefix, ps, n_free, pool, max_blocks, max_tokens;
 };
 
-struct Request {
-  int len, add, old_blocks, fresh;
-};
-
-// A request's lengths; out-of-range ones count as no new token (`bad` is set).
-__device__ __forceinline__ Request load_request(const PlanArgs& a, int b, bool& bad) {
-  int len = a.lens[b], add = a.news[b];
-  if (len < 0 || add < 0 || (int64_t)len + add + a.prefix > 0x7fffffff) {
-    bad = true;
-    len = max(len, 0);
-    add = 0;
-  }
-  Request r;
-  r.len = len;
-  r.add = add;
-  const unsigned ps = (unsigned)a.ps;
-  r.old_blocks = (int)(((unsigned)len + ps - 1) / ps);
-  r.fresh = (int)(((unsigned)len + (unsigned)add + ps - 1) / ps) - r.old_blocks;
-  return r;
+// x + y for 0 <= x, y < 2^31, held at 2^31 - 1 (associative, so a scan may use it): lengths come
+// from the caller's device memory, and a sum past 32 bits has to end as a recorded error.
+__device__ __forceinline__ int add_sat(int x, int y) {
+  return (int)min((unsigned)x + (unsigned)y, 0x7fffffffu);
 }
 
 // Largest b in [0, n) with sums[b] <= x (sums ascending, sums[0] = 0).
@@ -82,100 +67,100 @@ __device__ __forceinline__ int find_request(const int32_t* sums, int n, int x) {
 
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs a) {
   extern __shared__ int32_t plan_smem[];
-  int32_t* tok0 = plan_smem;         // [B] exclusive sum of new tokens (saturated)
-  int32_t* page0 = plan_smem + a.B;  // [B] exclusive sum of new pages (saturated)
-  __shared__ int64_t warp_tok[kPlanThreads / 32], warp_page[kPlanThreads / 32];
+  int32_t* len_s = plan_smem;                // [B] tokens before the step
+  int32_t* tok0 = plan_smem + a.B;           // [B + 1] exclusive sum of new tokens
+  int32_t* page0 = plan_smem + 2 * a.B + 1;  // [B] exclusive sum of new pages
+  __shared__ int2 warp_sum_s[kPlanThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned ps = (unsigned)a.ps;
   const int run = (a.B + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
+  const int cursor = a.cursor ? *a.cursor : 0;
 
   bool bad = false;
-  int64_t nt = 0, np = 0;
+  int nt = 0, np = 0;
   for (int b = b0; b < b1; ++b) {
-    const Request r = load_request(a, b, bad);
-    nt += r.add;
-    np += r.fresh;
+    int len = a.lens[b], add = a.news[b];
+    if (len < 0 || add < 0 || (int64_t)len + add + a.prefix > 0x7fffffff) {
+      bad = true;  // appends nothing
+      len = max(len, 0);
+      add = 0;
+    }
+    const int fresh = (int)(((unsigned)len + (unsigned)add + ps - 1) / ps - ((unsigned)len + ps - 1) / ps);
+    len_s[b] = len;
+    tok0[b] = add;
+    page0[b] = fresh;
+    nt = add_sat(nt, add);
+    np = add_sat(np, fresh);
   }
-  // block-wide exclusive scan in 64 bits (lengths come from the caller's device memory: their
-  // sum may pass 32 bits, which ends as a recorded error, not as a wrapped index)
-  int64_t st = nt, sp = np;
+  int st = nt, sp = np;  // inclusive over the warp, then over the warps
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t ut = __shfl_up_sync(0xffffffffu, st, o), up = __shfl_up_sync(0xffffffffu, sp, o);
+    const int ut = __shfl_up_sync(0xffffffffu, st, o), up = __shfl_up_sync(0xffffffffu, sp, o);
     if (lane >= o) {
-      st += ut;
-      sp += up;
+      st = add_sat(st, ut);
+      sp = add_sat(sp, up);
     }
   }
-  if (lane == 31) {
-    warp_tok[warp] = st;
-    warp_page[warp] = sp;
-  }
+  if (lane == 31) warp_sum_s[warp] = make_int2(st, sp);
   __syncthreads();
-  int64_t all_tok = 0, all_page = 0, t0 = 0, p0 = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w == warp) {
-      t0 = all_tok;
-      p0 = all_page;
-    }
-    all_tok += warp_tok[w];
-    all_page += warp_page[w];
+  int2 ws = lane < kPlanThreads / 32 ? warp_sum_s[lane] : make_int2(0, 0);
+#pragma unroll
+  for (int o = 1; o < kPlanThreads / 32; o <<= 1) {
+    const int ut = __shfl_up_sync(0xffffffffu, ws.x, o), up = __shfl_up_sync(0xffffffffu, ws.y, o);
+    if (lane >= o) ws = make_int2(add_sat(ws.x, ut), add_sat(ws.y, up));
   }
-  t0 += st - nt;
-  p0 += sp - np;
-  const int cursor = a.cursor ? *a.cursor : 0;
-  const int64_t kSat = 0x7fffffff;
+  const int all_tok = __shfl_sync(0xffffffffu, ws.x, kPlanThreads / 32 - 1);
+  const int all_page = __shfl_sync(0xffffffffu, ws.y, kPlanThreads / 32 - 1);
+  int t0 = __shfl_sync(0xffffffffu, ws.x, max(warp - 1, 0)), p0 = __shfl_sync(0xffffffffu, ws.y, max(warp - 1, 0));
+  const int et = __shfl_up_sync(0xffffffffu, st, 1), ep = __shfl_up_sync(0xffffffffu, sp, 1);
+  t0 = add_sat(warp ? t0 : 0, lane ? et : 0);
+  p0 = add_sat(warp ? p0 : 0, lane ? ep : 0);
   for (int b = b0; b < b1; ++b) {
-    bool dummy = false;
-    const Request r = load_request(a, b, dummy);
-    tok0[b] = (int32_t)min(t0, kSat);
-    page0[b] = (int32_t)min(p0, kSat);
-    t0 += r.add;
-    p0 += r.fresh;
+    const int add = tok0[b], fresh = page0[b];
+    tok0[b] = t0;
+    page0[b] = p0;
+    t0 = add_sat(t0, add);
+    p0 = add_sat(p0, fresh);
   }
+  if (tid == 0) tok0[a.B] = all_tok;
   __syncthreads();
 
   int error = bad || cursor < 0 ? VV_ERR_RANGE : 0;
   const int gtid = blockIdx.x * kPlanThreads + tid, gsize = gridDim.x * kPlanThreads;
-  const int n_tok = (int)min(all_tok, (int64_t)a.max_tokens);
+  const int n_tok = min(all_tok, a.max_tokens);
   if (all_tok > a.max_tokens) error = VV_ERR_CAPACITY;
   if (gtid == 0) {
     const int64_t end = (int64_t)cursor + all_page;
     if (end > a.n_free) error = VV_ERR_CAPACITY;
-    *a.cursor_out = (int32_t)min(end, kSat);
-    a.offsets[a.B] = n_tok;
+    *a.cursor_out = (int32_t)min(end, (int64_t)0x7fffffff);
   }
-  for (int b = gtid; b < a.B; b += gsize) {
-    bool dummy = false;
-    const Request r = load_request(a, b, dummy);
+  for (int b = gtid; b <= a.B; b += gsize) {
     a.offsets[b] = min(tok0[b], n_tok);
-    a.lens_out[b] = r.len + r.add;
+    if (b < a.B) a.lens_out[b] = len_s[b] + (tok0[b + 1] - tok0[b]);
   }
   // the page of fresh index p (over all requests), -1 when the list has run out or names no page
-  auto fresh_page = [&](int64_t p) {
-    const int64_t at = p + cursor;
+  auto fresh_page = [&](int p) {
+    const int64_t at = (int64_t)p + cursor;
     if (cursor < 0 || at >= a.n_free) return -1;
     const int page = a.free_pages[at];
     return page >= 0 && page < a.pool ? page : -1;
   };
-  const int n_page = (int)min(all_page, (int64_t)kSat);
-  for (int p = gtid; p < n_page; p += gsize) {
-    const int b = find_request(page0, a.B, p);
-    const int block = ((unsigned)a.lens[b] + (unsigned)a.ps - 1) / (unsigned)a.ps + (p - page0[b]);
-    const int page = fresh_page(p);
+  for (int64_t p = gtid; p < all_page; p += gsize) {
+    const int b = find_request(page0, a.B, (int)p);
+    const int block = (int)(((unsigned)len_s[b] + ps - 1) / ps) + ((int)p - page0[b]);
+    const int page = fresh_page((int)p);
     if (block < a.max_blocks)
       a.table[(int64_t)b * a.max_blocks + block] = page;
     else
       error = VV_ERR_CAPACITY;
-    if (page < 0 && error == 0) error = p + (int64_t)cursor >= a.n_free ? VV_ERR_CAPACITY : VV_ERR_RANGE;
-    if (gsize > 0x7fffffff - p) break;
+    if (page < 0 && error == 0) error = p + cursor >= a.n_free ? VV_ERR_CAPACITY : VV_ERR_RANGE;
   }
   // tokens, four in a row per thread: one bisection, then a walk
   for (int64_t t4 = (int64_t)gtid * 4; t4 < a.max_tokens; t4 += (int64_t)gsize * 4) {
     int64_t slot[4];
     int pos[4];
-    int b = -1, end = -1, page = -1, blk = -1;
-    Request r = {};
+    int b = -1, end = -1, first = 0, blk = -1, page = -1;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int t = (int)t4 + e;
@@ -183,28 +168,30 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
       pos[e] = 0;
       if (t >= n_tok) continue;
       if (t >= end) {
-        if (b < 0) {
+        if (b < 0)
           b = find_request(tok0, a.B, t);
-        } else {
+        else
           do ++b;
-          while (b + 1 < a.B && tok0[b + 1] <= t);
-        }
-        bool dummy = false;
-        r = load_request(a, b, dummy);
-        end = (int)min((int64_t)tok0[b] + r.add, kSat);
+          while (tok0[b + 1] <= t);
+        end = tok0[b + 1];
+        first = len_s[b] - tok0[b];
         blk = -1;
       }
-      const int i = r.len + (t - tok0[b]);
-      const int block = (int)((unsigned)i / (unsigned)a.ps);
+      const int i = first + t;
+      const int block = (int)((unsigned)i / ps);
       if (block != blk) {
         blk = block;
-        if (block >= r.old_blocks) {
-          page = block < a.max_blocks ? fresh_page((int64_t)page0[b] + (block - r.old_blocks)) : -1;
+        const int old = (int)(((unsigned)len_s[b] + ps - 1) / ps);
+        page = -1;
+        if (block >= a.max_blocks) {
+          if (error == 0) error = VV_ERR_CAPACITY;
+        } else if (block >= old) {
+          page = fresh_page(page0[b] + (block - old));
         } else {
-          page = block < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + block] : -1;
+          page = a.table[(int64_t)b * a.max_blocks + block];
           if (page < 0 || page >= a.pool) {
             page = -1;
-            if (error == 0) error = block < a.max_blocks ? VV_ERR_RANGE : VV_ERR_CAPACITY;
+            if (error == 0) error = VV_ERR_RANGE;
           }
         }
       }
@@ -240,6 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 // digit), then sine and cosine of the remainder in 32 bits.
 constexpr int kHeadDim = 128;
 constexpr int kRopeWarps = 8;
+constexpr int kRopeBatch = 4;  // loads of a warp in flight: 4 x 512 bytes
 
 struct RopeArgs {
   const void* q;
@@ -285,7 +273,7 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
 }
 
 template <typename T, bool GAINS>
-__global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_append_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 3) qk_rope_append_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 cs[kRopeWarps][kHeadDim / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t units = (int64_t)a.T * a.units_per_token;
@@ -331,49 +319,69 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_append_kernel(const _
     __syncwarp();
     float2 w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = cs[warp][(c & 7) * 8 + j];
-#pragma unroll 2
-    for (int pr = first; pr < last; ++pr) {
-      const int h = 2 * pr + row;
-      const bool live = h < heads;
-      const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
-      const int hk = is_k ? h - a.Hq : h - a.Hq - a.Hkv;
-      const T* src = is_q ? static_cast<const T*>(a.q) + t * a.q_stride + h * kHeadDim
-                          : (is_k ? static_cast<const T*>(a.k) + t * a.k_stride
-                                  : static_cast<const T*>(a.v) + t * a.v_stride) + hk * kHeadDim;
-      uint4 in = make_uint4(0, 0, 0, 0);
-      if (live && (is_q || write)) in = *reinterpret_cast<const uint4*>(src + c * 8);
-      float x[8];
-      const uint32_t iw[4] = {in.x, in.y, in.z, in.w};
+    for (int j = 0; j < 8; ++j) {
+      w[j] = cs[warp][(c & 7) * 8 + j];
+      w[j].y *= sign;
+    }
+    const T* q = static_cast<const T*>(a.q) + t * a.q_stride + c * 8;
+    const T* k = static_cast<const T*>(a.k) + t * a.k_stride + c * 8;
+    const T* v = static_cast<const T*>(a.v) + t * a.v_stride + c * 8;
+    T* q_out = static_cast<T*>(a.q_out) + t * a.qo_stride + c * 8;
+    T* kp = static_cast<T*>(a.kp) + cell + c * 8;
+    T* vp = static_cast<T*>(a.vp) + cell + c * 8;
+    for (int pr0 = first; pr0 < last; pr0 += kRopeBatch) {
+      uint4 in[kRopeBatch];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack2<T>(iw[j]);
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
+      for (int i = 0; i < kRopeBatch; ++i) {
+        const int h = 2 * (pr0 + i) + row;
+        const T* src = h < a.Hq ? q + h * kHeadDim
+                                : (h < a.Hq + a.Hkv ? k + (h - a.Hq) * kHeadDim : v + (h - a.Hq - a.Hkv) * kHeadDim);
+        in[i] = make_uint4(0, 0, 0, 0);
+        if (pr0 + i < last && h < heads && (h < a.Hq || write)) in[i] = *reinterpret_cast<const uint4*>(src);
       }
-      if (GAINS) {
-        float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+      for (int i = 0; i < kRopeBatch; ++i) {
+        const int h = 2 * (pr0 + i) + row;
+        if (pr0 + i >= last) break;
+        const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+        const uint32_t iw[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+        float x[8], other[8];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
-        const bool norm = is_q ? a.q_gain != nullptr : a.k_gain != nullptr;
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = unpack2<T>(iw[j]);
+          x[2 * j] = f.x;
+          x[2 * j + 1] = f.y;
+        }
+        if (GAINS) {
+          float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = norm ? x[j] * inv * (is_q ? qg[j] : kg[j]) : x[j];
+          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const bool norm = is_q ? a.q_gain != nullptr : a.k_gain != nullptr;
+          const float inv = norm ? rsqrtf(ss * (1.f / kHeadDim) + a.eps) : 1.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * (is_q ? qg[j] : kg[j]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) other[j] = __shfl_xor_sync(0xffffffffu, x[j], 8);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack2<T>(__shfl_xor_sync(0xffffffffu, iw[j], 8));
+            other[2 * j] = f.x;
+            other[2 * j + 1] = f.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], w[j].x, other[j] * w[j].y);
+        uint4 out = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+        T* dst = is_q ? q_out + h * kHeadDim : kp + (h - a.Hq) * a.head_stride;
+        if (!is_q && !is_k) {
+          out = in[i];
+          dst = vp + (h - a.Hq - a.Hkv) * a.head_stride;
+        }
+        if (h < heads && (is_q || write)) *reinterpret_cast<uint4*>(dst) = out;
       }
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float other = __shfl_xor_sync(0xffffffffu, x[j], 8);
-        y[j] = fmaf(x[j], w[j].x, sign * other * w[j].y);
-      }
-      uint4 out = make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]),
-                             pack2<T>(y[6], y[7]));
-      if (!is_q && !is_k) out = in;
-      T* dst = is_q ? static_cast<T*>(a.q_out) + t * a.qo_stride + h * kHeadDim
-                    : static_cast<T*>(is_k ? a.kp : a.vp) + cell + hk * a.head_stride;
-      if (live && (is_q || write)) *reinterpret_cast<uint4*>(dst + c * 8) = out;
     }
   }
 }
@@ -412,13 +420,13 @@ extern "C" vv_status vv_paged_plan(const int32_t* lens, const int32_t* new_lens,
   vv::PlanArgs a = {lens,  new_lens,   free_pages, cursor, block_tables, lens_out,
                     offsets, slots, positions, cursor_out, B, prefix_len,
                     page_size, n_free, pages, max_blocks, max_tokens};
-  const size_t smem = (size_t)B * 8;
+  const size_t smem = (size_t)B * 12 + 4;
   if (smem > (48u << 10))
     VV_CUDA(cudaFuncSetAttribute(vv::paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem));
-  // one CTA per 2048 tokens, at most one per SM (each repeats the scan)
+  // one CTA per 2048 tokens, at most three per SM (each repeats the scan)
   const int64_t per = vv::kPlanThreads * 4;
-  const int grid = (int)std::min<int64_t>(vv::sm_count(), ((int64_t)max_tokens + per - 1) / per);
+  const int grid = (int)std::min<int64_t>(3 * vv::sm_count(), ((int64_t)max_tokens + per - 1) / per);
   vv::paged_plan_kernel<<<grid, vv::kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   return vv::cuda_check(cudaGetLastError(), "vv_paged_plan launch");
 }
@@ -485,8 +493,8 @@ extern "C" vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const vo
   const int pairs = (Hq + 2 * Hkv + 1) / 2;
   const int64_t warps = (int64_t)vv::sm_count() * 32;
   const int64_t per = std::max<int64_t>(1, std::min<int64_t>(pairs, T * pairs / warps));
-  a.pairs_per_unit = (int)per;
   a.units_per_token = (int)((pairs + per - 1) / per);
+  a.pairs_per_unit = (pairs + a.units_per_token - 1) / a.units_per_token;  // equal shares
   const int64_t units = T * a.units_per_token;
   const int grid = (int)std::min<int64_t>((units + vv::kRopeWarps - 1) / vv::kRopeWarps,
                                           (int64_t)vv::sm_count() * 8);
