@@ -8,6 +8,7 @@
 // Softmax over the union of two key sets splits exactly: with (m, l, o) the maximum, the sum of
 // exp(s - m) and the weighted sum of values of each part, the union's are M = max(m_i),
 // L = sum l_i e^(m_i - M), O = sum o_i e^(m_i - M).
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -16,6 +17,7 @@
 #include <cmath>
 
 #include "attn_shared.h"
+#include "attn_tc.cuh"
 #include "vv_device.cuh"
 #include "vv_internal.h"
 
@@ -28,25 +30,40 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------------------------- own pages
 //
-// One CTA = one sequence, one key-value head, one of `splits` parts of the keys; its four warps
-// take chunks of 16 keys in turn, each through a ring of its own (cp.async, no CTA barrier in the
-// loop), so a page may end anywhere at a multiple of 16 and a warp waits for its own loads only.
-// The group's query heads (at most 16) are the rows of m16n8k16 products: S = Q K^T with the
-// chunk's keys as columns, O += P V with P straight from S's registers.  Decode attention reads
-// each key once for at most 16 query rows: 64 floating operations per byte at most, far below
-// what the warp-level matrix instruction sustains (about 250 per byte of HBM traffic), so the
-// loads are what counts and not the tensor path; a 128-row tile of the 5th-generation one would
-// be empty by 7/8 here.
-// Rows past the end of a sequence are filled with zeros by the copy itself (whatever a page holds
-// there, NaN included, never reaches the sums) and their scores are set to -inf.
-constexpr int kOwnWarps = 4;
-constexpr int kOwnThreads = kOwnWarps * 32;
-constexpr int kOwnStages = 3;
-constexpr int kChunk = 16;                            // keys per chunk
-constexpr int kChunkBytes = kChunk * D * 2;           // K or V of a chunk
-constexpr int kStageBytes = 2 * kChunkBytes;
-constexpr int kMinChunks = 16;                        // least chunks of a split
+// All keys of all sequences and key-value heads form one list of 16-key chunks, ordered by
+// sequence, head and position; the CTAs (one per SM) take equal runs of it, found from the lengths
+// on the device, so ragged batches load every SM alike (each head counts kEnd chunks more, what it
+// costs to finish one).  A head that lies in one run is finished by its CTA; one that crosses runs
+// leaves partial rows (at most two sets per CTA) and the last of its CTAs to arrive joins them in
+// run order: the result does not depend on who that is.
+//
+// One warp walks the run ahead of the others: eight lanes look up eight chunks' pages at a time
+// and copy their rows (TMA, 128-byte swizzle) into a ring of 21 chunks, 168 KB on their way per
+// SM; it runs across the ends of heads, so neither a new sequence's length and table nor the
+// joining of the last one leaves HBM idle.  Seven warps take the chunks in turn, each waiting for
+// its own chunk alone.
+// The group's query heads (at most 16) are the rows of m16n8k16 products: S = Q K^T with the keys
+// as columns, O += P V with P straight from S's registers.  Decode attention reads each key once
+// for at most 16 query rows, 64 floating operations per byte at most, far below what the
+// warp-level matrix instruction sustains, so the loads are what counts and not the tensor path; a
+// 128-row tile of the 5th-generation one would be empty by 7/8 here.
+// What a page holds behind a sequence's last key (NaN included) is kept out: those scores are set
+// to -inf and those rows of V to zero before the products.
+constexpr int kOwnWarps = 7;                          // consumers; one more warp copies
+constexpr int kOwnThreads = (kOwnWarps + 1) * 32;
+constexpr int kChunk = 16;                            // keys
+constexpr int kHalfBytes = kChunk * 128;              // 64 of the 128 dimensions of a chunk
+constexpr int kStageBytes = 4 * kHalfBytes;           // K then V
+constexpr int kOwnStages = 3 * kOwnWarps;              // a multiple: a stage has one consumer, which
+                                                      // sees each of its phases (a parity wait
+                                                      // must not be two phases behind)
+static_assert(kOwnStages % kOwnWarps == 0, "a stage belongs to one consumer warp");
+constexpr int kBatch = 8;                             // chunks copied at a time
+static_assert(kBatch <= kOwnStages, "a batch never waits for itself");
+constexpr int kEnd = 40;                              // a head's end, in chunks
+constexpr int kMinRun = 2 * kOwnWarps;                // least chunks of a run
 constexpr int kMinShared = 128;                       // least prompt with a kernel of its own
+constexpr int kOwnSmem = kOwnStages * kStageBytes + kOwnWarps * 8 * kPartRow * 4 + 1024;
 
 struct SharedAttnArgs {
   const void* q;
@@ -58,12 +75,12 @@ struct SharedAttnArgs {
   const int32_t* lens;
   void* out;
   float* lse;
-  float* part;       // [B][Hkv][splits][G][kPartRow]: this kernel's parts
-  unsigned* arrived; // [B][Hkv]
+  float* part;       // [CTAs][2][G][kPartRow]: a run's first head (begun in an earlier run), its last
+  unsigned* arrived; // [CTAs]: arrivals for the head that begins in this run and goes on
   const float* pre_part;  // [Hkv][pre_splits][B * G][kPartRow]: the shared prompt's
   int pre_splits;    // 0: the prompt's keys, if any, are read here (kpre, vpre, P)
   int64_t q_stride, out_stride, pre_head, pre_token, page_stride, head_stride, token_stride;
-  int B, Hkv, G, P, ps, pages, max_blocks, splits;
+  int B, Hkv, G, P, ps, pages, max_blocks;
   float c;  // scale * log2(e)
 };
 
@@ -101,330 +118,419 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// 16 bytes global -> shared; `bytes` = 0 writes zeros and reads nothing
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ float exp2_fast(float x) {  // -inf -> 0; its error is far below a half step of T
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kOwnThreads) own_attn_kernel(const __grid_constant__ SharedAttnArgs a) {
-  extern __shared__ __align__(128) unsigned char osm[];
-  __shared__ int s_last;
-  const int split = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.G;
-  const int raw_len = a.lens[b];
-  if (raw_len < 0) {  // padding row
-    pdl_wait();
-    return;
-  }
-  const int cap = (int)min((int64_t)a.max_blocks * a.ps, (int64_t)0x7fffffff);
-  const int len = min(raw_len, cap);
-  if (raw_len > cap && tid == 0 && split == 0 && g == 0) set_device_error(VV_ERR_CAPACITY);
+// Copies a chunk of K or of V: both halves of 64 dimensions, 16 rows each.
+__device__ __forceinline__ void tma_chunk(uint32_t dst, const CUtensorMap* tm, int token, int head, int page,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %2, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(token), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
 
-  // chunks: the prompt's first, then the sequence's own
-  const int npre = a.pre_splits ? 0 : (a.P + kChunk - 1) / kChunk;
-  const int nch = npre + (len + kChunk - 1) / kChunk;
-  const int per = max((nch + a.splits - 1) / a.splits, kMinChunks);
-  const int active = max((nch + per - 1) / per, 1);
-  if (split >= active) {
-    pdl_wait();
-    return;
-  }
-  const int c0 = split * per, c1 = min(c0 + per, nch);
+struct OwnMaps {
+  CUtensorMap k, v;        // pages: dims {64, page_size, 2, Hkv, pages}, box {64, 16, 2, 1, 1}
+  CUtensorMap kpre, vpre;  // prompt: dims {64, P, 2, Hkv, 1}, the same box; rows past P read as zeros
+};
 
-  const T* kpre = static_cast<const T*>(a.kpre) + (int64_t)g * a.pre_head;
-  const T* vpre = static_cast<const T*>(a.vpre) + (int64_t)g * a.pre_head;
-  const T* kp = static_cast<const T*>(a.kp) + (int64_t)g * a.head_stride;
-  const T* vp = static_cast<const T*>(a.vp) + (int64_t)g * a.head_stride;
-  const int32_t* tbl = a.table + (int64_t)b * a.max_blocks;
-  const uint32_t ring = smem_u32(osm) + warp * (kOwnStages * kStageBytes);
+// The CTA of n whose run of a list of `total` places holds place x (run c: [total c / n, total (c + 1) / n)).
+__device__ __forceinline__ int run_of(int64_t x, int64_t total, int n) {
+  int c = (int)(x * n / total);
+  while (total * (c + 1) / n <= x) ++c;
+  while (total * c / n > x) --c;
+  return c;
+}
 
-  // the group's queries as A fragments, 8 steps of 16 dimensions; rows past G are zero
-  uint32_t qf[8][4];
-  {
-    const int r = lane >> 2, kc = (lane & 3) * 2;
-    const T* q0 = static_cast<const T*>(a.q) + (int64_t)b * a.q_stride + (int64_t)g * G * D;
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = r + (e & 1) * 8, col = s * 16 + kc + (e >> 1) * 8;
-        qf[s][e] = row < G ? *reinterpret_cast<const uint32_t*>(q0 + row * D + col) : 0u;
-      }
-    }
-  }
+// Where a warp is in its CTA's run: chunk t of `chunks` of head g of sequence b.
+struct Walker {
+  int b, g, t, chunks, len;
+};
+// A row's joined parts, four dimensions a lane.
+struct Joined {
+  float m, l;
+  float4 o;
+};
 
-  // page of own chunk c (-1: none); the lookup runs a chunk ahead of the copy that uses it
-  auto page_of = [&](int c) {
-    if (c < npre || c >= c1) return 0;
-    return tbl[(c - npre) * kChunk / a.ps];
-  };
-  // copies chunk c into ring slot st; returns the number of its keys
-  auto issue = [&](int c, int st, int page) {
-    const T *ks, *vs;
-    int64_t step;
-    int keys;
-    if (c < npre) {
-      keys = min(a.P - c * kChunk, kChunk);
-      ks = kpre + (int64_t)c * kChunk * a.pre_token;
-      vs = vpre + (int64_t)c * kChunk * a.pre_token;
-      step = a.pre_token;
-    } else {
-      const int p0 = (c - npre) * kChunk;
-      keys = min(len - p0, kChunk);
-      if (page < 0 || page >= a.pages) {
-        keys = 0;
-        page = 0;
-        if (lane == 0) set_device_error(VV_ERR_RANGE);
-      }
-      const int64_t at = (int64_t)page * a.page_stride + (int64_t)(p0 % a.ps) * a.token_stride;
-      ks = kp + at;
-      vs = vp + at;
-      step = a.token_stride;
+// Joins n parts of a row into r; part k lies at base + k * stride: o[128], m, l.  The maxima and sums
+// of up to KB parts are read one a lane and their rows together, one round trip to L2 a batch.
+template <int KB>
+__device__ __forceinline__ void absorb(Joined& r, const float* base, int n, int64_t stride, int lane) {
+  for (int k0 = 0; k0 < n; k0 += KB) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < KB && k0 + lane < n) ml = *reinterpret_cast<const float2*>(base + (k0 + lane) * stride + D);
+    float4 v[KB];
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k < n) v[k] = *reinterpret_cast<const float4*>(base + (k0 + k) * stride + lane * 4);
     }
-    const uint32_t dst = ring + st * kStageBytes;
+    const float mn = fmaxf(r.m, warp_max(ml.x)), ref = mn == -INFINITY ? 0.f : mn;
+    const float w0 = exp2_fast(r.m - ref), w = exp2_fast(ml.x - ref);
+    r.m = mn;
+    r.l = r.l * w0 + warp_sum(w * ml.y);
+    r.o = make_float4(r.o.x * w0, r.o.y * w0, r.o.z * w0, r.o.w * w0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = i * 2 + (lane >> 4), c16 = lane & 15;
-      const uint32_t n = row < keys ? 16u : 0u;
-      const int64_t off = (row < keys ? row : 0) * step + c16 * 8;
-      const uint32_t d = dst + row * 256 + ((c16 ^ (row & 7)) << 4);
-      cp16(d, ks + off, n);
-      cp16(d + kChunkBytes, vs + off, n);
+    for (int k = 0; k < KB; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      r.o = make_float4(fmaf(wk, v[k].x, r.o.x), fmaf(wk, v[k].y, r.o.y), fmaf(wk, v[k].z, r.o.z), fmaf(wk, v[k].w, r.o.w));
     }
-    return keys;
-  };
-  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-
-  float o[16][4];
-#pragma unroll
-  for (int n = 0; n < 16; ++n) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-  }
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  int keys[kOwnStages];
-  int c_issue = c0 + warp;
-  int page = page_of(c_issue);
-#pragma unroll
-  for (int s = 0; s < kOwnStages - 1; ++s) {
-    const int next = page_of(c_issue + kOwnWarps);
-    keys[s] = c_issue < c1 ? issue(c_issue, s, page) : 0;
-    commit();
-    page = next;
-    c_issue += kOwnWarps;
-  }
-  int st = 0, st_in = kOwnStages - 1;
-  for (int ch = c0 + warp; ch < c1; ch += kOwnWarps) {
-    const int next = page_of(c_issue + kOwnWarps);
-    int k_in = 0;
-    if (c_issue < c1) k_in = issue(c_issue, st_in, page);
-    commit();
-    page = next;
-    c_issue += kOwnWarps;
-#pragma unroll
-    for (int s = 0; s < kOwnStages; ++s)
-      if (s == st_in) keys[s] = k_in;
-    asm volatile("cp.async.wait_group %0;" ::"n"(kOwnStages - 1) : "memory");
-    __syncwarp();
-    int n_keys = 0;
-#pragma unroll
-    for (int s = 0; s < kOwnStages; ++s)
-      if (s == st) n_keys = keys[s];
-    const uint32_t kt = ring + st * kStageBytes, vt = kt + kChunkBytes;
-
-    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-    {
-      const int row = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        uint32_t r[4];
-        ldsm4(r, kt + row * 256 + (((s * 2 + half) ^ (row & 7)) << 4));
-        mma16816<T>(s0, qf[s], r[0], r[1]);
-        mma16816<T>(s1, qf[s], r[2], r[3]);
-      }
-    }
-    // s0: keys 2 (lane % 4) + {0, 1} of rows lane / 4 and lane / 4 + 8; s1: the same, keys + 8
-    const int col = (lane & 3) * 2;
-    float x[2][4];
-    x[0][0] = col < n_keys ? s0[0] * a.c : -INFINITY;
-    x[0][1] = col + 1 < n_keys ? s0[1] * a.c : -INFINITY;
-    x[0][2] = col + 8 < n_keys ? s1[0] * a.c : -INFINITY;
-    x[0][3] = col + 9 < n_keys ? s1[1] * a.c : -INFINITY;
-    x[1][0] = col < n_keys ? s0[2] * a.c : -INFINITY;
-    x[1][1] = col + 1 < n_keys ? s0[3] * a.c : -INFINITY;
-    x[1][2] = col + 8 < n_keys ? s1[2] * a.c : -INFINITY;
-    x[1][3] = col + 9 < n_keys ? s1[3] * a.c : -INFINITY;
-    float corr[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[h], mx);
-      const float ref = mn == -INFINITY ? 0.f : mn;  // nothing above -inf yet: all weights 0
-      corr[h] = exp2_fast(m[h] - ref);
-      m[h] = mn;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[h][e] = exp2_fast(x[h][e] - ref);
-      l[h] = l[h] * corr[h] + ((x[h][0] + x[h][1]) + (x[h][2] + x[h][3]));
-    }
-    if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
-#pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        o[n][0] *= corr[0];
-        o[n][1] *= corr[0];
-        o[n][2] *= corr[1];
-        o[n][3] *= corr[1];
-      }
-    }
-    const uint32_t p[4] = {pack_pair<T>(x[0][0], x[0][1]), pack_pair<T>(x[1][0], x[1][1]),
-                           pack_pair<T>(x[0][2], x[0][3]), pack_pair<T>(x[1][2], x[1][3])};
-    {
-      const int row = lane & 15, half = lane >> 4;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        uint32_t r[4];
-        ldsm4t(r, vt + row * 256 + (((n * 2 + half) ^ (row & 7)) << 4));
-        mma16816<T>(o[2 * n], p, r[0], r[1]);
-        mma16816<T>(o[2 * n + 1], p, r[2], r[3]);
-      }
-    }
-    __syncwarp();
-    st = st + 1 == kOwnStages ? 0 : st + 1;
-    st_in = st_in + 1 == kOwnStages ? 0 : st_in + 1;
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
-
-  // the warps' partials meet in shared memory (over the rings)
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-  }
-  float* sp = reinterpret_cast<float*>(osm);  // [warps][G][kPartRow]
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = (lane >> 2) + h * 8;
-    if (row < G) {
-      float* d = sp + (warp * G + row) * kPartRow;
-#pragma unroll
-      for (int n = 0; n < 16; ++n)
-        *reinterpret_cast<float2*>(d + n * 8 + (lane & 3) * 2) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
-      if ((lane & 3) == 0) {
-        d[D] = m[h];
-        d[D + 1] = l[h];
-      }
-    }
-  }
-  __syncthreads();
-  // A warp joins a row at a time, four dimensions a lane.  Of each set of parts the maxima and sums
-  // are read 32 at a time, one a lane, then the rows one after the other: two round trips to L2
-  // for up to 32 parts.
-  struct Joined {
-    float m, l;
-    float4 o;
-  };
-  auto absorb = [&](Joined& r, const float* parts, int n, int64_t stride) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int cnt = min(n - i0, 32);
-      const float* base = parts + i0 * stride;
-      const float2 ml = lane < cnt ? *reinterpret_cast<const float2*>(base + lane * stride + D)
-                                   : make_float2(-INFINITY, 0.f);
-      const float mn = fmaxf(r.m, warp_max(ml.x)), ref = mn == -INFINITY ? 0.f : mn;
-      const float w0 = exp2_fast(r.m - ref), w = exp2_fast(ml.x - ref);
-      r.m = mn;
-      r.l = r.l * w0 + warp_sum(lane < cnt ? w * ml.y : 0.f);
-      r.o = make_float4(r.o.x * w0, r.o.y * w0, r.o.z * w0, r.o.w * w0);
-#pragma unroll 4
-      for (int i = 0; i < cnt; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        const float4 v = *reinterpret_cast<const float4*>(base + i * stride + lane * 4);
-        r.o = make_float4(fmaf(wi, v.x, r.o.x), fmaf(wi, v.y, r.o.y), fmaf(wi, v.z, r.o.z), fmaf(wi, v.w, r.o.w));
-      }
-    }
-  };
-  const int64_t item = (int64_t)b * a.Hkv + g;
-  float* part = a.part + item * a.splits * G * kPartRow;
-  if (active > 1) {
-    for (int row = warp; row < G; row += kOwnWarps) {
-      Joined r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      absorb(r, sp + row * kPartRow, kOwnWarps, (int64_t)G * kPartRow);
-      float* d = part + ((int64_t)split * G + row) * kPartRow;
-      *reinterpret_cast<float4*>(d + lane * 4) = r.o;
-      if (lane == 0) *reinterpret_cast<float2*>(d + D) = make_float2(r.m, r.l);
-    }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(&a.arrived[item], 1u) == (unsigned)(active - 1);
-    __syncthreads();
-    if (!s_last) {
-      pdl_wait();
-      return;
-    }
-    __threadfence();
-    if (tid == 0) a.arrived[item] = 0;
-  }
-  pdl_wait();  // the prompt's parts are complete
-  for (int row = warp; row < G; row += kOwnWarps) {
-    Joined r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (active > 1)
-      absorb(r, part + row * kPartRow, active, (int64_t)G * kPartRow);
-    else
-      absorb(r, sp + row * kPartRow, kOwnWarps, (int64_t)G * kPartRow);
-    const int64_t rows = (int64_t)a.B * G;
-    absorb(r, a.pre_part + ((int64_t)g * a.pre_splits * rows + (int64_t)b * G + row) * kPartRow, a.pre_splits, rows * kPartRow);
-    const int h = g * G + row;
-    // l is 0 where no key has a weight; a NaN score makes l NaN and goes on to the result
-    const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
-    T* dst = static_cast<T*>(a.out) + (int64_t)b * a.out_stride + h * D + lane * 4;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_pair<T>(r.o.x * inv, r.o.y * inv), pack_pair<T>(r.o.z * inv, r.o.w * inv));
-    if (a.lse && lane == 0)
-      a.lse[(int64_t)b * a.Hkv * G + h] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
   }
 }
 
-// Parts per (sequence, head): enough CTAs for two per SM, none with fewer than kMinChunks chunks.
-int own_splits(int B, int Hkv, int64_t keys) {
-  const int64_t want = std::max<int64_t>(1, 2 * sm_count() / std::max<int64_t>(1, (int64_t)B * Hkv));
-  const int64_t most = std::max<int64_t>(1, (keys + kChunk * kMinChunks - 1) / (kChunk * kMinChunks));
-  return (int)std::min<int64_t>({want, most, 64});
+template <typename T, bool WIDE>  // WIDE: 9 to 16 query heads per key-value head
+__global__ void __launch_bounds__(kOwnThreads, 1)
+    own_attn_kernel(const __grid_constant__ OwnMaps mp, const __grid_constant__ SharedAttnArgs a) {
+  extern __shared__ __align__(1024) unsigned char osm_raw[];
+  unsigned char* osm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(osm_raw) + 1023) & ~uintptr_t(1023));
+  float* sp = reinterpret_cast<float*>(osm + kOwnStages * kStageBytes);  // [warps][8 rows][kPartRow]
+  __shared__ __align__(8) uint64_t full[kOwnStages], empty[kOwnStages];
+  __shared__ int64_t warp_sum_s[kOwnThreads / 32];
+  __shared__ Walker s_first;
+  __shared__ int s_bad[kOwnStages];  // the chunk's page does not exist
+  __shared__ int s_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.G;
+  const int cap = (int)min((int64_t)a.max_blocks * a.ps, (int64_t)0x7fffffff);
+  const int npre = a.pre_splits ? 0 : (a.P + kChunk - 1) / kChunk;
+  if (tid < kOwnStages) {
+    mbar_init(&full[tid], 1);
+    mbar_init(&empty[tid], 1);
+    fence_mbar_init();
+  }
+  // chunks of a sequence, per head: a sequence without keys has one empty chunk (its rows are
+  // written by whoever holds it), a padding row none
+  auto chunks_of = [&](int len) { return len < 0 ? 0 : max(npre + (min(len, cap) + kChunk - 1) / kChunk, 1); };
+  auto places_of = [&](int chunks) { return chunks ? (int64_t)chunks + kEnd : 0; };
+  const int per = (a.B + kOwnThreads - 1) / kOwnThreads;
+  const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);
+  int64_t mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += places_of(chunks_of(a.lens[b]));
+  int64_t scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += u;
+  }
+  if (lane == 31) warp_sum_s[warp] = scan;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kOwnThreads / 32; ++w) {
+    if (w < warp) before += warp_sum_s[w];
+    total += warp_sum_s[w];
+  }
+  before = (before + scan - mine) * a.Hkv;  // places before this thread's sequences
+  total *= a.Hkv;
+  // runs: all CTAs, or fewer when the list is short
+  const int n_run = (int)min((int64_t)gridDim.x, max(total / (kMinRun + kEnd), (int64_t)1));
+  const int cta = blockIdx.x;
+  if (total == 0 || cta >= n_run) {
+    pdl_wait();
+    return;
+  }
+  const int64_t x0 = total * cta / n_run, x1 = total * (cta + 1) / n_run;
+  if (before <= x0 && x0 < before + mine * a.Hkv) {
+    int64_t at = before;
+    for (int b = b_lo;; ++b) {
+      const int len = a.lens[b], chunks = chunks_of(len);
+      const int64_t places = places_of(chunks);
+      if (x0 < at + places * a.Hkv) {
+        int g = 0;
+        for (at += places; at <= x0; at += places) ++g;
+        s_first = {b, g, (int)(x0 - (at - places)), chunks, len};
+        break;
+      }
+      at += places * a.Hkv;
+    }
+  }
+  __syncthreads();
+  // the parts of heads in this run: f(walker, place of chunk walker.t, chunks here, chunks before)
+  auto for_each_head = [&](auto&& f) {
+    Walker w = s_first;
+    int64_t x = x0;
+    int c = 0;
+    while (true) {
+      if (w.t < w.chunks) {
+        const int n = (int)min((int64_t)(w.chunks - w.t), x1 - x);
+        f(w, x, n, c);
+        c += n;
+      }
+      x += places_of(w.chunks) - w.t;
+      if (x >= x1) return;
+      w.t = 0;
+      if (++w.g == a.Hkv) {
+        w.g = 0;
+        do {
+          w.len = a.lens[++w.b];
+          w.chunks = chunks_of(w.len);
+        } while (w.chunks == 0);
+      }
+    }
+  };
+
+  if (warp == kOwnWarps) {
+    for_each_head([&](const Walker& w, int64_t, int n, int c) {
+      if (w.t == 0 && w.g == 0 && w.len > cap && lane == 0) set_device_error(VV_ERR_CAPACITY);
+      const int n_own = min(w.len, cap);
+      // lane's chunk of the batch that begins with chunk i: its page, -1 where there is nothing to copy
+      auto page_of = [&](int i) {
+        const int t = w.t + i + lane;
+        if (lane >= kBatch || i + lane >= n) return -1;
+        if (t < npre) return 0;
+        const int p0 = (t - npre) * kChunk;
+        if (p0 >= n_own) return -1;
+        int page = a.table[(int64_t)w.b * a.max_blocks + p0 / a.ps];
+        if (page < 0 || page >= a.pages) {
+          set_device_error(VV_ERR_RANGE);
+          page = -2;
+        }
+        return page;
+      };
+      int page = page_of(0);
+      for (int i = 0; i < n; i += kBatch) {
+        const int next = page_of(i + kBatch);  // looked up while this batch waits and is copied
+        if (lane < kBatch && i + lane < n) {
+          const int t = w.t + i + lane, at = c + i + lane, st = at % kOwnStages, used = at / kOwnStages;
+          // the stage's chunk before was copied by an earlier batch: this wait ends by itself
+          if (used > 0) tc::wait_phase(&empty[st], (used - 1) & 1);
+          s_bad[st] = page == -2;
+          mbar_arrive_expect_tx(&full[st], page >= 0 ? kStageBytes : 0);
+          if (page >= 0) {
+            const bool pre = t < npre;
+            const int p0 = (pre ? t : t - npre) * kChunk, tok = pre ? p0 : p0 % a.ps;
+            const uint32_t s0 = smem_u32(osm + st * kStageBytes);
+            tma_chunk(s0, pre ? &mp.kpre : &mp.k, tok, w.g, page, &full[st]);
+            tma_chunk(s0 + 2 * kHalfBytes, pre ? &mp.vpre : &mp.v, tok, w.g, page, &full[st]);
+          }
+        }
+        __syncwarp();
+        page = next;
+      }
+    });
+    pdl_wait();
+    return;
+  }
+
+  auto consumers_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kOwnWarps * 32) : "memory"); };
+  bool waited = false;  // for the prompt's kernel
+  for_each_head([&](const Walker& w, int64_t x, int n, int c) {
+    // the group's queries as A fragments, 8 steps of 16 dimensions; rows past G are zero
+    uint32_t qf[8][4];
+    {
+      const int r = lane >> 2, kc = (lane & 3) * 2;
+      const T* q0 = static_cast<const T*>(a.q) + (int64_t)w.b * a.q_stride + (int64_t)w.g * G * D;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = r + (e & 1) * 8, col = s * 16 + kc + (e >> 1) * 8;
+          qf[s][e] = (WIDE || !(e & 1)) && row < G ? *reinterpret_cast<const uint32_t*>(q0 + row * D + col) : 0u;
+        }
+      }
+    }
+    float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    }
+    for (int i = (warp + kOwnWarps - c % kOwnWarps) % kOwnWarps; i < n; i += kOwnWarps) {
+      const int st = (c + i) % kOwnStages, t = w.t + i;
+      int n_keys = min(t < npre ? a.P - t * kChunk : min(w.len, cap) - (t - npre) * kChunk, kChunk);
+      tc::wait_phase(&full[st], ((c + i) / kOwnStages) & 1);
+      if (s_bad[st]) n_keys = 0;
+      if (n_keys > 0) {
+        const uint32_t kt = smem_u32(osm + st * kStageBytes), vt = kt + 2 * kHalfBytes;
+        if (n_keys < kChunk) {
+          // zero what the page holds behind the last key, 16 bytes a lane
+          for (int z = lane + n_keys * 8; z < kChunk * 8; z += 32) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + z * 16), "r"(0) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + kHalfBytes + z * 16), "r"(0) : "memory");
+          }
+          __syncwarp();
+        }
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        {
+          const int row = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            uint32_t r[4];
+            ldsm4(r, kt + (s >> 2) * kHalfBytes + row * 128 + ((((s & 3) * 2 + half) ^ (row & 7)) << 4));
+            mma16816<T>(sc[0], qf[s], r[0], r[1]);
+            mma16816<T>(sc[1], qf[s], r[2], r[3]);
+          }
+        }
+        // sc[0]: keys 2 (lane % 4) + {0, 1} of rows lane / 4 and lane / 4 + 8; sc[1]: the same, keys + 8
+        if (n_keys < kChunk) {
+          const int col = (lane & 3) * 2;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (col + (e & 1) >= n_keys) sc[0][e] = -INFINITY;
+            if (col + (e & 1) + 8 >= n_keys) sc[1][e] = -INFINITY;
+          }
+        }
+        float corr[2] = {1.f, 1.f};
+        uint32_t p[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
+          float mx = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[h], mx * a.c);
+          const float ref = mn == -INFINITY ? 0.f : mn;  // nothing above -inf yet: all weights 0
+          corr[h] = exp2_fast(m[h] - ref);
+          m[h] = mn;
+          const float w0 = exp2_fast(fmaf(sc[0][2 * h], a.c, -ref)), w1 = exp2_fast(fmaf(sc[0][2 * h + 1], a.c, -ref));
+          const float w2 = exp2_fast(fmaf(sc[1][2 * h], a.c, -ref)), w3 = exp2_fast(fmaf(sc[1][2 * h + 1], a.c, -ref));
+          l[h] = l[h] * corr[h] + ((w0 + w1) + (w2 + w3));
+          p[h] = pack_pair<T>(w0, w1);
+          p[h + 2] = pack_pair<T>(w2, w3);
+        }
+        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            o[k][0] *= corr[0];
+            o[k][1] *= corr[0];
+            o[k][2] *= corr[1];
+            o[k][3] *= corr[1];
+          }
+        }
+        {
+          const int row = lane & 15, half = lane >> 4;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t r[4];
+            ldsm4t(r, vt + (k >> 2) * kHalfBytes + row * 128 + ((((k & 3) * 2 + half) ^ (row & 7)) << 4));
+            mma16816<T>(o[2 * k], p, r[0], r[1]);
+            mma16816<T>(o[2 * k + 1], p, r[2], r[3]);
+          }
+        }
+        if (n_keys < kChunk) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next copy
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+
+    // ---- the head ends here, or goes on in the next run: which runs share it
+    int c0 = cta, parts = 1;
+    const int64_t h0 = x - w.t, h1 = h0 + w.chunks;
+    if (h0 < x0) c0 = run_of(h0, total, n_run);
+    if (h0 < x0 || h1 > x1) parts = (h1 > x1 ? run_of(h1 - 1, total, n_run) : cta) - c0 + 1;
+    float* part = a.part + ((int64_t)cta * 2 + (c0 == cta ? 1 : 0)) * G * kPartRow;
+    const int64_t all = (int64_t)a.B * G;
+    const float* pre = a.pre_part + ((int64_t)w.g * a.pre_splits * all + (int64_t)w.b * G) * kPartRow;
+    auto finish = [&](Joined& r, int row) {
+      if (!waited) {
+        pdl_wait();  // the prompt's parts are complete
+        waited = true;
+      }
+      absorb<16>(r, pre + row * kPartRow, a.pre_splits, all * kPartRow, lane);
+      const int h = w.g * G + row;
+      // l is 0 where no key has a weight; a NaN score makes l NaN and goes on to the result
+      const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+      T* dst = static_cast<T*>(a.out) + (int64_t)w.b * a.out_stride + h * D + lane * 4;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_pair<T>(r.o.x * inv, r.o.y * inv), pack_pair<T>(r.o.z * inv, r.o.w * inv));
+      if (a.lse && lane == 0)
+        a.lse[(int64_t)w.b * a.Hkv * G + h] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
+    };
+    // join the warps' rows through shared memory, eight rows at a time, a row per warp
+#pragma unroll
+    for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
+      if (h == 1) consumers_sync();  // the first eight have been read
+      float* d = sp + (warp * 8 + (lane >> 2)) * kPartRow;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        *reinterpret_cast<float2*>(d + k * 8 + (lane & 3) * 2) = make_float2(o[k][2 * h], o[k][2 * h + 1]);
+      if ((lane & 3) == 0) *reinterpret_cast<float2*>(d + D) = make_float2(m[h], l[h]);
+      consumers_sync();
+      for (int row = warp; row < min(G - 8 * h, 8); row += kOwnWarps) {
+        Joined r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        absorb<kOwnWarps>(r, sp + row * kPartRow, kOwnWarps, 8 * kPartRow, lane);
+        if (parts == 1) {
+          finish(r, 8 * h + row);
+        } else {
+          float* to = part + (8 * h + row) * kPartRow;
+          *reinterpret_cast<float4*>(to + lane * 4) = r.o;
+          if (lane == 0) *reinterpret_cast<float2*>(to + D) = make_float2(r.m, r.l);
+        }
+      }
+    }
+    if (parts > 1) {
+      __threadfence();
+      consumers_sync();
+      if (tid == 0) s_last = atomicAdd(&a.arrived[c0], 1u) == (unsigned)(parts - 1);
+      consumers_sync();
+      if (s_last) {
+        __threadfence();
+        if (tid == 0) a.arrived[c0] = 0;
+        for (int row = warp; row < G; row += kOwnWarps) {
+          Joined r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+          // the set that c0 began last, then the first sets of the CTAs after it
+          const float* p0 = a.part + ((int64_t)c0 * 2 * G + row) * kPartRow;
+          absorb<1>(r, p0 + G * kPartRow, 1, 0, lane);
+          absorb<16>(r, p0 + 2 * G * kPartRow, parts - 1, 2 * (int64_t)G * kPartRow, lane);
+          finish(r, row);
+        }
+      }
+    }
+    consumers_sync();  // the join buffer is free again
+  });
+  if (!waited) pdl_wait();
 }
 
 struct Plan {
-  int splits, pre_splits, pre_per;
+  int ctas, pre_splits, pre_per;
   size_t part, pre_part, total;  // byte offsets in the workspace; the arrival counters come first
 };
 Plan plan_of(int B, int Hkv, int G, int P, int64_t max_own) {
   Plan p = {};
   // One sequence shares nothing, and a prompt of a few chunks costs less to read again than a
-  // second kernel: there the prompt's keys are the first chunks of every sequence.
+  // second kernel: there the prompt's keys are the first tiles of every sequence.
   const bool shared = B > 1 && P >= kMinShared;
   if (shared) prefix_tc_split(B * G, Hkv, P, &p.pre_splits, &p.pre_per);
-  p.splits = own_splits(B, Hkv, max_own + (shared ? 0 : P));
+  const int64_t chunks = (max_own + kChunk - 1) / kChunk + (shared ? 0 : (P + kChunk - 1) / kChunk);
+  p.ctas = (int)std::min<int64_t>(sm_count(), std::max<int64_t>(chunks, 1) * B * Hkv);
   const size_t row = kPartRow * sizeof(float);
-  p.part = ((size_t)B * Hkv * 4 + 255) / 256 * 256;
-  p.pre_part = p.part + (p.splits > 1 ? (size_t)B * Hkv * p.splits * G * row : 0);
+  p.part = ((size_t)p.ctas * 4 + 255) / 256 * 256;
+  p.pre_part = p.part + (size_t)p.ctas * 2 * G * row;
   p.total = p.pre_part + (size_t)p.pre_splits * B * Hkv * G * row;
   return p;
 }
 
-template <typename T>
-cudaError_t launch_own(const SharedAttnArgs& a, cudaStream_t s) {
-  const size_t smem = std::max<size_t>(kOwnWarps * kOwnStages * kStageBytes,
-                                       (size_t)kOwnWarps * a.G * kPartRow * 4);
-  cudaError_t e = cudaFuncSetAttribute(own_attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+// Tensor map of rows of D elements, the two halves of a row as a dimension of their own so that
+// one copy fills both swizzled halves of a chunk: dims {64, tokens, 2, heads, pages}, box
+// {64, 16, 2, 1, 1}.
+bool page_map(CUtensorMap* tm, const void* base, int dtype, int64_t tokens, int64_t heads, int64_t pages,
+              int64_t token_stride, int64_t head_stride, int64_t page_stride) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[5] = {64, (cuuint64_t)tokens, 2, (cuuint64_t)heads, (cuuint64_t)pages};
+  // the stride of a dimension of one element is never used, but has to be a valid one
+  cuuint64_t strides[4] = {(cuuint64_t)token_stride * 2, 128, (cuuint64_t)(heads > 1 ? head_stride : token_stride) * 2,
+                           (cuuint64_t)(pages > 1 ? page_stride : token_stride) * 2};
+  cuuint32_t box[5] = {64, kChunk, 2, 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(tm, dtype == VV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, bool WIDE>
+cudaError_t launch_own(const OwnMaps& mp, const SharedAttnArgs& a, int ctas, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(own_attn_kernel<T, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem);
   if (e != cudaSuccess) return e;
-  return launch(own_attn_kernel<T>, dim3(a.splits, a.Hkv, a.B), dim3(kOwnThreads), smem, s,
-                a.pre_splits > 0, a);
+  return launch(own_attn_kernel<T, WIDE>, dim3(ctas), dim3(kOwnThreads), kOwnSmem, s, a.pre_splits > 0, mp, a);
 }
 
 bool sizes_ok(int B, int Hq, int Hkv, int D_, int P) {
@@ -507,7 +613,6 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
   a.ps = kv->page_size;
   a.pages = kv->pages;
   a.max_blocks = max_blocks;
-  a.splits = p.splits;
   a.c = scale * vv::kLog2e;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.pre_splits) {
@@ -529,6 +634,16 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
     t.dtype = kv->dtype;
     VV_CUDA(vv::launch_prefix_tc(t, s));
   }
-  const cudaError_t e = kv->dtype == VV_F16 ? vv::launch_own<__half>(a, s) : vv::launch_own<__nv_bfloat16>(a, s);
+  vv::OwnMaps mp = {};
+  bool ok = vv::page_map(&mp.k, kv->k, kv->dtype, kv->page_size, Hkv, kv->pages, kv->token_stride, kv->head_stride, kv->page_stride) &&
+            vv::page_map(&mp.v, kv->v, kv->dtype, kv->page_size, Hkv, kv->pages, kv->token_stride, kv->head_stride, kv->page_stride);
+  if (ok && prefix_len > 0 && !p.pre_splits)
+    ok = vv::page_map(&mp.kpre, k_prefix, kv->dtype, prefix_len, Hkv, 1, prefix_token_stride, prefix_head_stride, 0) &&
+         vv::page_map(&mp.vpre, v_prefix, kv->dtype, prefix_len, Hkv, 1, prefix_token_stride, prefix_head_stride, 0);
+  if (!ok) return vv::set_error(VV_ERR_CUDA, "vv_gqa_prefix_attn: tensor map encoding failed");
+  const bool f16 = kv->dtype == VV_F16, wide = G > 8;
+  const cudaError_t e = f16 ? (wide ? vv::launch_own<__half, true>(mp, a, p.ctas, s) : vv::launch_own<__half, false>(mp, a, p.ctas, s))
+                            : (wide ? vv::launch_own<__nv_bfloat16, true>(mp, a, p.ctas, s)
+                                    : vv::launch_own<__nv_bfloat16, false>(mp, a, p.ctas, s));
   return vv::cuda_check(e, "vv_gqa_prefix_attn launch");
 }

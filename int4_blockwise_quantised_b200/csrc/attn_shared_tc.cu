@@ -78,15 +78,6 @@ __device__ __forceinline__ uint32_t pack_w<__nv_bfloat16>(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A wait of this kernel is some hundred cycles; the bounded wait reads the global timer first, which
-// costs more than that.  So a few plain tries (each sleeps in hardware for a while) come first.
-__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try_wait(bar, parity)) return;
-  mbar_wait(bar, parity);
-}
-
 struct KvMaps {
   CUtensorMap k, v;  // dims {D, P, Hkv}, box {64, 128, 1}; rows past P read as zeros
 };
@@ -283,6 +274,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_row[s][r] = m_new;
         asm volatile("bar.arrive %0, 64;" ::"r"(2 + quarter * 2 + s) : "memory");
       }
+      // P_{j-2} has been read.  Its product also comes after that of block j - 3, so the other
+      // group's barrier is in the phase of block j - 1 from here until P_j is handed over: the
+      // rescaling below can wait for that phase by its parity
+      if (j > 1) wait_phase(&pv_done[s], ((j >> 1) - 1) & 1);
       if (j > 0 && __any_sync(0xffffffffu, move)) {
         const float corr = move ? ex2_approx(m_prev - m_new) : 1.f;
         wait_phase(&pv_done[s ^ 1], ((j - 1) >> 1) & 1);  // O holds the blocks before
@@ -300,7 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float ref = m_new == -INFINITY ? 0.f : m_new;  // nothing above -inf yet: weights 0
       l *= ex2_approx(m_mine - ref);
       m_mine = m_new;
-      if (j > 1) wait_phase(&pv_done[s], ((j >> 1) - 1) & 1);  // P_{j-2} has been read
       float ls0 = 0.f, ls1 = 0.f;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -373,16 +367,15 @@ cudaError_t launch_t(const KvMaps& mp, const PrefixTcArgs& a, cudaStream_t s) {
 }  // namespace
 
 void prefix_tc_split(int rows, int Hkv, int P, int* splits, int* per) {
-  // as many parts as fill one wave of the SMs, of equally many 128-key blocks; with more tiles
-  // than SMs, the number of parts (up to 8) whose last wave wastes least, at about two blocks'
-  // time for a part's start and end
+  // Cost in blocks of 128 keys (about 0.85 us each): waves x (a part's blocks + 4 for its start and
+  // end), and 1/16 for each part that the second kernel has to join.
   const int64_t tiles = (int64_t)((rows + BM - 1) / BM) * Hkv, sms = sm_count();
   const int blocks = (P + BN - 1) / BN;
   int64_t best = INT64_MAX;
   const int most = (int)std::min<int64_t>(blocks, std::max<int64_t>(8, sms / tiles));
   for (int s = 1; s <= most; ++s) {
     const int p = (blocks + s - 1) / s, used = (blocks + p - 1) / p;
-    const int64_t cost = (tiles * used + sms - 1) / sms * (p + 2);
+    const int64_t cost = (tiles * used + sms - 1) / sms * (p + 4) * 16 + used;
     if (cost < best) {
       best = cost;
       *splits = used;

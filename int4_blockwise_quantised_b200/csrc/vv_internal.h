@@ -47,10 +47,12 @@ inline vv_status check_paged_kv(const vv_paged_kv* kv, int Hkv, int D, const cha
                      (int64_t)kv->pages * kv->page_size < (int64_t(1) << 31),
                  "%s: %d pages of %d tokens (page size a multiple of 16)", who, kv->pages,
                  kv->page_size);
-  VV_CHECK_SHAPE(kv->page_stride >= 0 && kv->head_stride >= 0 && kv->token_stride >= D &&
-                     kv->page_stride % 8 == 0 && kv->head_stride % 8 == 0 &&
-                     kv->token_stride % 8 == 0,
-                 "%s: page strides must be non-negative multiples of 8 elements", who);
+  const int64_t most = int64_t(1) << 38;  // of a tensor map, in elements
+  VV_CHECK_SHAPE((kv->pages == 1 || kv->page_stride >= D) && (Hkv == 1 || kv->head_stride >= D) &&
+                     kv->token_stride >= D && kv->page_stride % 8 == 0 && kv->head_stride % 8 == 0 &&
+                     kv->token_stride % 8 == 0 && kv->page_stride < most && kv->head_stride < most &&
+                     kv->token_stride < most,
+                 "%s: page strides must be multiples of 8 elements, at least %d and below 2^38", who, D);
   return VV_OK;
 }
 
