@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         if (lane < kBatch && i + lane < n) {
           const int t = w.t + i + lane, at = c + i + lane, st = at % kOwnStages, used = at / kOwnStages;
           // the stage's chunk before was copied by an earlier batch: this wait ends by itself
-          if (used > 0) tc::wait_phase(&empty[st], (used - 1) & 1);
+          if (used > 0) wait_phase(&empty[st], (used - 1) & 1);
           s_bad[st] = page == -2;
           mbar_arrive_expect_tx(&full[st], page >= 0 ? kStageBytes : 0);
           if (page >= 0) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
     for (int i = (warp + kOwnWarps - c % kOwnWarps) % kOwnWarps; i < n; i += kOwnWarps) {
       const int st = (c + i) % kOwnStages, t = w.t + i;
       int n_keys = min(t < npre ? a.P - t * kChunk : min(w.len, cap) - (t - npre) * kChunk, kChunk);
-      tc::wait_phase(&full[st], ((c + i) / kOwnStages) & 1);
+      wait_phase(&full[st], ((c + i) / kOwnStages) & 1);
       if (s_bad[st]) n_keys = 0;
       if (n_keys > 0) {
         const uint32_t kt = smem_u32(osm + st * kStageBytes), vt = kt + 2 * kHalfBytes;

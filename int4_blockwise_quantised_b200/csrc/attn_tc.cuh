@@ -16,23 +16,6 @@ namespace tc {
 constexpr uint32_t kTile = 128 * 128 * 2;  // one 128 x 128 tile of 16-bit elements: two 64-column atoms
 constexpr uint32_t kAtom = 128 * 128;      // 128 rows x 128 bytes
 
-// Bounded wait for short phases: plain tries (each sleeps in hardware for a moment), the time limit
-// looked at every 256 of them.  mbar_wait reads the global timer before its first retry and then
-// sleeps up to 20 us at a time: after some microseconds of waiting it wakes microseconds late.
-__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity) {
-  uint64_t t0 = 0;
-#pragma unroll 1
-  for (unsigned i = 1; !mbar_try_wait(bar, parity); ++i) {
-    if ((i & 255) != 0) continue;
-    if (t0 == 0) {
-      t0 = globaltimer_ns();
-    } else if (wait_expired(t0, kWaitLimitNs)) {
-      set_device_error(VV_ERR_TIMEOUT);
-      return;
-    }
-  }
-}
-
 // K-major, 128-byte swizzle: SBO = 1024 (8 rows x 128 B)
 __device__ __forceinline__ uint64_t desc_k_sw128(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |

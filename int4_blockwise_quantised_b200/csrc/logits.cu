@@ -72,7 +72,7 @@ __device__ __forceinline__ unsigned ordered_bits(float x) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const __grid_constant__ LogitsArgs a) {
+__global__ void __launch_bounds__(kLogitThreads, 3) logits_process_kernel(const __grid_constant__ LogitsArgs a) {
   constexpr int VEC = 16 / sizeof(T);   // elements of a 16-byte load
   constexpr int NV = kPer / VEC;        // such loads per thread
   extern __shared__ __align__(16) unsigned char lsm[];
@@ -102,6 +102,18 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const __g
     }
   }
 
+  const float rep = history && a.r.repetition ? a.r.repetition[b] : 1.f;
+  const float freq = history && a.r.frequency ? a.r.frequency[b] : 0.f;
+  const float pres = history && a.r.presence ? a.r.presence[b] : 0.f;
+  const uint32_t* mask = a.r.mask ? a.r.mask + (int64_t)b * a.r.mask_stride : nullptr;
+  unsigned allow[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    // the first of VEC (4 or 8) tokens is a multiple of it: their bits lie in one word
+    const int e0 = v0 + (j * kLogitThreads + tid) * VEC;
+    allow[j] = mask && e0 < a.V ? mask[e0 >> 5] >> (e0 & 31) : 0xffffffffu;
+  }
+
   // which tokens of the run the history and the biases name: one bit each, so that nothing else has
   // to be cleared, and a run of logits without any is only masked and copied
   bool bad = false;
@@ -129,17 +141,23 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const __g
       volatile unsigned* word = &bits[which][d >> 5];
       if (!((*word >> (d & 31)) & 1)) atomicOr(&bits[which][d >> 5], 1u << (d & 31));
     };
-#pragma unroll 4
-    for (int i = tid; i < plen; i += kLogitThreads) {
-      const unsigned d = (unsigned)tok[i] - (unsigned)v0;
-      if (d < (unsigned)nv) mark(kSeen, d);
-    }
-#pragma unroll 2
-    for (int i = plen + tid; i < len; i += kLogitThreads) {
-      const unsigned d = (unsigned)tok[i] - (unsigned)v0;
-      if (d < (unsigned)nv) {
-        mark(kSaid, d);
-        count[d] = 0;
+    constexpr int kMany = 4;  // ids of a thread on their way at once
+    for (int j0 = 0; j0 < len; j0 += kMany * kLogitThreads) {
+      unsigned t[kMany];
+#pragma unroll
+      for (int j = 0; j < kMany; ++j) {
+        const int i = j0 + j * kLogitThreads + tid;
+        t[j] = i < len ? (unsigned)tok[i] - (unsigned)v0 : 0xffffffffu;
+      }
+#pragma unroll
+      for (int j = 0; j < kMany; ++j) {
+        if (t[j] >= (unsigned)nv) continue;
+        if (j0 + j * kLogitThreads + tid < plen) {
+          mark(kSeen, t[j]);
+        } else {
+          mark(kSaid, t[j]);
+          count[t[j]] = 0;
+        }
       }
     }
     for (int i = i0 + tid; i < i1; i += kLogitThreads) {
@@ -165,17 +183,12 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const __g
     __syncthreads();
   }
 
-  const float rep = history && a.r.repetition ? a.r.repetition[b] : 1.f;
-  const float freq = history && a.r.frequency ? a.r.frequency[b] : 0.f;
-  const float pres = history && a.r.presence ? a.r.presence[b] : 0.f;
-  const uint32_t* mask = a.r.mask ? a.r.mask + (int64_t)b * a.r.mask_stride : nullptr;
   unsigned long long best = 0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e0 = (j * kLogitThreads + tid) * VEC;
     if (e0 >= nv) continue;
-    // e0 is a multiple of VEC (4 or 8): its bits lie in one word
-    const unsigned allowed = mask ? mask[(v0 + e0) >> 5] >> ((v0 + e0) & 31) : 0xffffffffu;
+    const unsigned allowed = allow[j];
     unsigned seen = 0, said = 0, named = 0;
     if (history || biased) {
       seen = bits[kSeen][e0 >> 5] >> (e0 & 31);

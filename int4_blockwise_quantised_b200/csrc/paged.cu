@@ -219,32 +219,34 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 //   (x_i, x_{i+64}) <- (x_i c - x_{i+64} s, x_{i+64} c + x_i s),  angle = pos * theta^(-2i/128)
 //
 // Bound by HBM: every head row is read once and written once (512 bytes for 128 elements, about
-// 30 floating operations per 4 bytes).  Half a warp holds one head row, 16 bytes a lane, so a
-// warp's load covers two rows; a lane's rotation partner is the lane 8 further on, and the squares
-// of a row are summed over its 16 lanes.  The angles of a token are found once per warp and
-// shared by all heads it handles: two frequencies a lane, the turns pos * theta^(-2i/128) / 2 pi
-// reduced to [-1/2, 1/2] in 64 bits (in 32 bits a position of 10^6 would lose the angle's second
-// digit), then sine and cosine of the remainder in 32 bits.
+// 40 instructions per 32 bytes).  A unit is one token's heads, or a part of them; a warp works alone
+// on its units and has the next two on their way (cp.async.bulk into a ring of its own, a token's
+// heads of one kind are contiguous): about 150 KB per SM with 16 warps, whatever their registers,
+// and no barrier between warps.  Half a warp turns one head row, 16 bytes a lane; the rotation's
+// partner is read from shared memory too.  A token's angles are found once per unit, two a lane: the
+// turns pos * theta^(-2i/128) / 2 pi reduced to [-1/2, 1/2] in 64 bits (in 32 bits a position of
+// 10^6 would lose the angle's second digit), then sine and cosine of the remainder in 32 bits.
 constexpr int kHeadDim = 128;
 constexpr int kRopeWarps = 8;
-constexpr int kRopeBatch = 4;  // loads of a warp in flight: 4 x 512 bytes
+constexpr int kRopeStages = 3;
+constexpr int kRopeHeads = 18;  // most heads of a unit: 8 warps x 3 x 4.5 KB, two CTAs per SM
 
 struct RopeArgs {
-  const void* q;
-  const void* k;
-  const void* v;
-  void* q_out;
-  void* kp;
-  void* vp;
+  const char* q;
+  const char* k;
+  const char* v;
+  char* q_out;
+  char* kp;
+  char* vp;
   const void* q_gain;
   const void* k_gain;
   const int32_t* pos;
   const int64_t* slots;
-  int64_t q_stride, k_stride, v_stride, qo_stride;
-  int64_t page_stride, head_stride, token_stride;
+  int64_t q_stride, k_stride, v_stride, qo_stride;        // bytes
+  int64_t page_stride, head_stride, token_stride;         // bytes
   int64_t n_slots;
   int T, Hq, Hkv, ps;
-  int pairs_per_unit, units_per_token;
+  int heads, parts;  // heads per unit; units per token
   float eps;
   double turns[kHeadDim / 2];  // theta^(-2i/D) / (2 pi)
 };
@@ -273,115 +275,144 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
 }
 
 template <typename T, bool GAINS>
-__global__ void __launch_bounds__(kRopeWarps * 32, 3) qk_rope_append_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float2 cs[kRopeWarps][kHeadDim / 2];
+__global__ void __launch_bounds__(kRopeWarps * 32, 2) qk_rope_append_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(128) unsigned char ring_all[];
+  __shared__ __align__(8) uint64_t full_all[kRopeWarps][kRopeStages];
+  __shared__ __align__(16) float2 cs_all[kRopeWarps][kHeadDim / 2];
+  constexpr int kRow = kHeadDim * 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t units = (int64_t)a.T * a.units_per_token;
-  const int heads = a.Hq + 2 * a.Hkv, pairs = (heads + 1) / 2;
-  const int c = lane & 15, row = lane >> 4;  // 16-byte chunk of the row; which row of the pair
+  const int n_heads = a.Hq + 2 * a.Hkv, unit_bytes = a.heads * kRow;
+  unsigned char* ring = ring_all + warp * (kRopeStages * unit_bytes);
+  uint64_t* full = full_all[warp];
+  float2* cs = cs_all[warp];
+  if (lane == 0) {
+    for (int i = 0; i < kRopeStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const int64_t units = (int64_t)a.T * a.parts, step = (int64_t)gridDim.x * kRopeWarps;
+  const int64_t u0 = (int64_t)blockIdx.x * kRopeWarps + warp;
+  // lane p copies the unit's queries (p = 0), keys or values
+  const char* src = lane == 0 ? a.q : lane == 1 ? a.k : a.v;
+  const int64_t stride = lane == 0 ? a.q_stride : lane == 1 ? a.k_stride : a.v_stride;
+  const int lo = lane == 0 ? 0 : a.Hq + (lane - 1) * a.Hkv, hi = lane == 0 ? a.Hq : lo + a.Hkv;
+  auto copy = [&](int64_t u, int st) {
+    if (u >= units) return;
+    const int t = (int)(u / a.parts), h0 = (int)(u - (int64_t)t * a.parts) * a.heads, nh = min(a.heads, n_heads - h0);
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], nh * kRow);
+    __syncwarp();
+    const int from = max(lo, h0), to = min(hi, h0 + nh);
+    if (lane < 3 && from < to)
+      bulk_g2s(ring + st * unit_bytes + (from - h0) * kRow, src + t * stride + (from - lo) * kRow, (to - from) * kRow,
+               &full[st]);
+  };
+#pragma unroll
+  for (int i = 0; i < kRopeStages; ++i) copy(u0 + i * step, i);
+
+  const int c = lane & 15;  // 16-byte piece of the row
   const float sign = c < 8 ? -1.f : 1.f;
-  const double f0 = a.turns[lane], f1 = a.turns[lane + 32];
-  float qg[8], kg[8];
+  uint32_t qg[4], qo[4], kg[4], ko[4];  // gains of this piece and of its partner
   if (GAINS) {
+    const uint32_t one = pack2<T>(1.f, 1.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 one = make_float2(1.f, 1.f);
-      const float2 x = a.q_gain ? unpack2<T>(reinterpret_cast<const uint32_t*>(a.q_gain)[c * 4 + j]) : one;
-      const float2 y = a.k_gain ? unpack2<T>(reinterpret_cast<const uint32_t*>(a.k_gain)[c * 4 + j]) : one;
-      qg[2 * j] = x.x;
-      qg[2 * j + 1] = x.y;
-      kg[2 * j] = y.x;
-      kg[2 * j + 1] = y.y;
+      const uint32_t *gq = static_cast<const uint32_t*>(a.q_gain), *gk = static_cast<const uint32_t*>(a.k_gain);
+      qg[j] = gq ? gq[c * 4 + j] : one;
+      qo[j] = gq ? gq[(c ^ 8) * 4 + j] : one;
+      kg[j] = gk ? gk[c * 4 + j] : one;
+      ko[j] = gk ? gk[(c ^ 8) * 4 + j] : one;
     }
   }
-  for (int64_t u = (int64_t)blockIdx.x * kRopeWarps + warp; u < units; u += (int64_t)gridDim.x * kRopeWarps) {
-    const int t = (int)(u / a.units_per_token);
-    const int first = (int)(u - (int64_t)t * a.units_per_token) * a.pairs_per_unit;
-    const int last = min(first + a.pairs_per_unit, pairs);
-    const double p = (double)a.pos[t];
-    const int64_t slot = a.slots[t];
-    bool write = slot >= 0;
-    if (slot >= a.n_slots) {
-      write = false;
-      if (lane == 0) set_device_error(VV_ERR_RANGE);
-    }
-    const int64_t page = write ? slot / a.ps : 0;
-    const int64_t cell = page * a.page_stride + (write ? slot - page * a.ps : 0) * a.token_stride;
-    __syncwarp();
+  const double f0 = a.turns[lane], f1 = a.turns[lane + 32];
+  int pos = 0;
+  int64_t slot = -1;
+  if (u0 < units) {
+    pos = a.pos[u0 / a.parts];
+    slot = a.slots[u0 / a.parts];
+  }
+  int st = 0;
+  uint32_t round = 0;
+  for (int64_t u = u0; u < units; u += step) {
+    const int t = (int)(u / a.parts), h0 = (int)(u - (int64_t)t * a.parts) * a.heads, nh = min(a.heads, n_heads - h0);
     {
-      const double x0 = p * f0, x1 = p * f1;
-      float s, co;
-      sincospif(2.f * (float)(x0 - rint(x0)), &s, &co);
-      cs[warp][lane] = make_float2(co, s);
-      sincospif(2.f * (float)(x1 - rint(x1)), &s, &co);
-      cs[warp][lane + 32] = make_float2(co, s);
+      const double x0 = (double)pos * f0, x1 = (double)pos * f1;
+      float sn, cn;
+      sincospif(2.f * (float)(x0 - rint(x0)), &sn, &cn);
+      cs[lane] = make_float2(cn, sn);
+      sincospif(2.f * (float)(x1 - rint(x1)), &sn, &cn);
+      cs[lane + 32] = make_float2(cn, sn);
+    }
+    int64_t at = -1;  // byte offset of the token's cell in the pool
+    if (slot >= a.n_slots) {
+      if (lane == 0) set_device_error(VV_ERR_RANGE);
+    } else if (slot >= 0) {
+      const int page = (int)slot / a.ps;
+      at = page * a.page_stride + ((int)slot - page * a.ps) * a.token_stride;
+    }
+    if (u + step < units) {  // the next unit's
+      pos = a.pos[(u + step) / a.parts];
+      slot = a.slots[(u + step) / a.parts];
     }
     __syncwarp();
     float2 w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[j] = cs[warp][(c & 7) * 8 + j];
-      w[j].y *= sign;
+    for (int j = 0; j < 8; j += 2) {
+      const float4 f = *reinterpret_cast<const float4*>(&cs[(c & 7) * 8 + j]);
+      w[j] = make_float2(f.x, f.y * sign);
+      w[j + 1] = make_float2(f.z, f.w * sign);
     }
-    const T* q = static_cast<const T*>(a.q) + t * a.q_stride + c * 8;
-    const T* k = static_cast<const T*>(a.k) + t * a.k_stride + c * 8;
-    const T* v = static_cast<const T*>(a.v) + t * a.v_stride + c * 8;
-    T* q_out = static_cast<T*>(a.q_out) + t * a.qo_stride + c * 8;
-    T* kp = static_cast<T*>(a.kp) + cell + c * 8;
-    T* vp = static_cast<T*>(a.vp) + cell + c * 8;
-    for (int pr0 = first; pr0 < last; pr0 += kRopeBatch) {
-      uint4 in[kRopeBatch];
-#pragma unroll
-      for (int i = 0; i < kRopeBatch; ++i) {
-        const int h = 2 * (pr0 + i) + row;
-        const T* src = h < a.Hq ? q + h * kHeadDim
-                                : (h < a.Hq + a.Hkv ? k + (h - a.Hq) * kHeadDim : v + (h - a.Hq - a.Hkv) * kHeadDim);
-        in[i] = make_uint4(0, 0, 0, 0);
-        if (pr0 + i < last && h < heads && (h < a.Hq || write)) in[i] = *reinterpret_cast<const uint4*>(src);
+    wait_phase(&full[st], round & 1);
+    const unsigned char* in = ring + st * unit_bytes;
+#pragma unroll 2
+    for (int r = lane >> 4; r < ((nh + 1) & ~1); r += 2) {
+      const bool live = r < nh;
+      const int head = h0 + r;
+      const bool is_q = head < a.Hq, is_k = !is_q && head < a.Hq + a.Hkv;
+      uint4 own = make_uint4(0, 0, 0, 0), par = own;
+      if (live) {
+        own = *reinterpret_cast<const uint4*>(in + r * kRow + c * 16);
+        par = *reinterpret_cast<const uint4*>(in + r * kRow + (c ^ 8) * 16);
       }
+      const uint32_t ow[4] = {own.x, own.y, own.z, own.w}, pw[4] = {par.x, par.y, par.z, par.w};
+      float x[8], y[8];
 #pragma unroll
-      for (int i = 0; i < kRopeBatch; ++i) {
-        const int h = 2 * (pr0 + i) + row;
-        if (pr0 + i >= last) break;
-        const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
-        const uint32_t iw[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-        float x[8], other[8];
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<T>(ow[j]), g = unpack2<T>(pw[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+        y[2 * j] = g.x;
+        y[2 * j + 1] = g.y;
+      }
+      if (GAINS) {
+        float ss = 0.f, inv = 1.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (is_q ? a.q_gain != nullptr : a.k_gain != nullptr) inv = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 f = unpack2<T>(iw[j]);
-          x[2 * j] = f.x;
-          x[2 * j + 1] = f.y;
+          const float2 f = unpack2<T>(is_q ? qg[j] : kg[j]), g = unpack2<T>(is_q ? qo[j] : ko[j]);
+          x[2 * j] *= inv * f.x;
+          x[2 * j + 1] *= inv * f.y;
+          y[2 * j] *= inv * g.x;
+          y[2 * j + 1] *= inv * g.y;
         }
-        if (GAINS) {
-          float ss = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const bool norm = is_q ? a.q_gain != nullptr : a.k_gain != nullptr;
-          const float inv = norm ? rsqrtf(ss * (1.f / kHeadDim) + a.eps) : 1.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * (is_q ? qg[j] : kg[j]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) other[j] = __shfl_xor_sync(0xffffffffu, x[j], 8);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack2<T>(__shfl_xor_sync(0xffffffffu, iw[j], 8));
-            other[2 * j] = f.x;
-            other[2 * j + 1] = f.y;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], w[j].x, other[j] * w[j].y);
-        uint4 out = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
-        T* dst = is_q ? q_out + h * kHeadDim : kp + (h - a.Hq) * a.head_stride;
-        if (!is_q && !is_k) {
-          out = in[i];
-          dst = vp + (h - a.Hq - a.Hkv) * a.head_stride;
-        }
-        if (h < heads && (is_q || write)) *reinterpret_cast<uint4*>(dst) = out;
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], w[j].x, y[j] * w[j].y);
+      uint4 out = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+      if (!is_q && !is_k) out = own;
+      char* dst = is_q ? a.q_out + t * a.qo_stride + head * kRow
+                       : is_k ? a.kp + at + (head - a.Hq) * a.head_stride
+                              : a.vp + at + (head - a.Hq - a.Hkv) * a.head_stride;
+      if (live && (is_q || at >= 0)) *reinterpret_cast<uint4*>(dst + c * 16) = out;
+    }
+    __syncwarp();
+    copy(u + kRopeStages * step, st);
+    if (++st == kRopeStages) {
+      st = 0;
+      ++round;
     }
   }
 }
@@ -462,55 +493,50 @@ extern "C" vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const vo
                    o0 + o_bytes <= q0,
                "vv_qk_rope_append: q_out must be q itself (same stride) or not overlap it");
   vv::RopeArgs a;
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.q_out = q_out;
-  a.kp = kv->k;
-  a.vp = kv->v;
+  a.q = static_cast<const char*>(q);
+  a.k = static_cast<const char*>(k);
+  a.v = static_cast<const char*>(v);
+  a.q_out = static_cast<char*>(q_out);
+  a.kp = static_cast<char*>(kv->k);
+  a.vp = static_cast<char*>(kv->v);
   a.q_gain = q_gain;
   a.k_gain = k_gain;
   a.pos = positions;
   a.slots = slots;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.qo_stride = q_out_stride;
-  a.page_stride = kv->page_stride;
-  a.head_stride = kv->head_stride;
-  a.token_stride = kv->token_stride;
+  a.q_stride = q_stride * 2;
+  a.k_stride = k_stride * 2;
+  a.v_stride = v_stride * 2;
+  a.qo_stride = q_out_stride * 2;
+  a.page_stride = kv->page_stride * 2;
+  a.head_stride = kv->head_stride * 2;
+  a.token_stride = kv->token_stride * 2;
   a.n_slots = (int64_t)kv->pages * kv->page_size;
   a.T = (int)T;
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.ps = kv->page_size;
   a.eps = eps;
-  // theta^(-2i/D) by repeated use of one logarithm in double: relative error of a few 2^-53
   const double kTwoPi = 6.283185307179586476925286766559;
   for (int i = 0; i < D / 2; ++i) a.turns[i] = std::pow((double)theta, -2.0 * i / D) / kTwoPi;
-  // a warp takes pairs_per_unit pairs of heads of one token: all of them when there are tokens
-  // enough for every warp slot, fewer when the batch is a step of a few tokens
-  const int pairs = (Hq + 2 * Hkv + 1) / 2;
-  const int64_t warps = (int64_t)vv::sm_count() * 32;
-  const int64_t per = std::max<int64_t>(1, std::min<int64_t>(pairs, T * pairs / warps));
-  a.units_per_token = (int)((pairs + per - 1) / per);
-  a.pairs_per_unit = (pairs + a.units_per_token - 1) / a.units_per_token;  // equal shares
-  const int64_t units = T * a.units_per_token;
-  const int grid = (int)std::min<int64_t>((units + vv::kRopeWarps - 1) / vv::kRopeWarps,
-                                          (int64_t)vv::sm_count() * 8);
+  // a token in as few units of at most 18 heads as there are warps for, in smaller ones (an even
+  // number of heads, two rows at a time) when tokens are few
+  const int heads = Hq + 2 * Hkv;
+  const int64_t warps = 2 * vv::sm_count() * vv::kRopeWarps;
+  int64_t parts = (heads + vv::kRopeHeads - 1) / vv::kRopeHeads;
+  parts = std::max(parts, std::min<int64_t>((heads + 1) / 2, warps / T));
+  a.heads = (int)((heads + parts - 1) / parts + 1) / 2 * 2;
+  a.parts = (heads + a.heads - 1) / a.heads;
+  const int64_t units = T * a.parts;
+  const int grid = (int)std::min<int64_t>((units + vv::kRopeWarps - 1) / vv::kRopeWarps, 2 * vv::sm_count());
+  const size_t smem = (size_t)vv::kRopeWarps * vv::kRopeStages * a.heads * D * 2;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool gains = q_gain || k_gain;
-  const dim3 block(vv::kRopeWarps * 32);
-  if (kv->dtype == VV_KV_F16) {
-    if (gains)
-      vv::qk_rope_append_kernel<__half, true><<<grid, block, 0, s>>>(a);
-    else
-      vv::qk_rope_append_kernel<__half, false><<<grid, block, 0, s>>>(a);
-  } else {
-    if (gains)
-      vv::qk_rope_append_kernel<__nv_bfloat16, true><<<grid, block, 0, s>>>(a);
-    else
-      vv::qk_rope_append_kernel<__nv_bfloat16, false><<<grid, block, 0, s>>>(a);
-  }
+  auto kernel = kv->dtype == VV_F16
+                    ? (gains ? vv::qk_rope_append_kernel<__half, true> : vv::qk_rope_append_kernel<__half, false>)
+                    : (gains ? vv::qk_rope_append_kernel<__nv_bfloat16, true>
+                             : vv::qk_rope_append_kernel<__nv_bfloat16, false>);
+  if (smem > (40u << 10))
+    VV_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  kernel<<<grid, vv::kRopeWarps * 32, smem, s>>>(a);
   return vv::cuda_check(cudaGetLastError(), "vv_qk_rope_append launch");
 }

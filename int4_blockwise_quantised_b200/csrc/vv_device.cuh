@@ -118,6 +118,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   return true;
 }
 
+// Bounded wait for short phases: plain tries (each sleeps in hardware for a moment), the time limit
+// looked at every 256 of them.  mbar_wait reads the global timer before its first retry and then
+// sleeps up to 20 us at a time: after some microseconds of waiting it wakes microseconds late.
+__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (unsigned i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 255) != 0) continue;
+    if (t0 == 0) {
+      t0 = globaltimer_ns();
+    } else if (wait_expired(t0, kWaitLimitNs)) {
+      set_device_error(VV_ERR_TIMEOUT);
+      return;
+    }
+  }
+}
+
 __device__ __forceinline__ uint32_t ld_acquire_u32(const unsigned* p) {
   uint32_t v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
