@@ -28,8 +28,8 @@
 namespace vv {
 namespace {
 
-constexpr int kLogitThreads = 512;
-constexpr int kPer = 16;                        // logits per thread, in registers
+constexpr int kLogitThreads = 256;
+constexpr int kPer = 32;                        // logits per thread, in registers
 constexpr int kSlice = kLogitThreads * kPer;    // 8192 tokens of a row per CTA
 
 struct RowBest {
@@ -45,7 +45,8 @@ struct LogitsArgs {
   vv_logits_rules r;
   int32_t* argmax;
   RowBest* ws;
-  int V, words;
+  int V;
+  bool packed;  // counts and biases share a word
 };
 
 template <typename T>
@@ -71,17 +72,30 @@ __device__ __forceinline__ unsigned ordered_bits(float x) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+// A load that stays where it is written (the compiler moves plain ones down to their use).
+__device__ __forceinline__ unsigned load_now(const int32_t* p) {
+  unsigned v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kLogitThreads, 3) logits_process_kernel(const __grid_constant__ LogitsArgs a) {
+__global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const __grid_constant__ LogitsArgs a) {
   constexpr int VEC = 16 / sizeof(T);   // elements of a 16-byte load
   constexpr int NV = kPer / VEC;        // such loads per thread
   extern __shared__ __align__(16) unsigned char lsm[];
   __shared__ unsigned long long warp_key[kLogitThreads / 32];
+  constexpr int kNear = 2;  // biases of a thread in registers
+  __shared__ float bias_val[kNear * kLogitThreads];
   const bool history = a.r.tokens != nullptr, biased = a.r.bias_ids != nullptr;
-  unsigned* count = reinterpret_cast<unsigned*>(lsm);                              // [kSlice]
-  unsigned* bias = reinterpret_cast<unsigned*>(lsm + (history ? kSlice * 4 : 0));  // [kSlice]
-  __shared__ unsigned bits[3][kSlice / 32];
-  constexpr int kSeen = 0, kSaid = 1, kBias = 2;
+  // per token of the run: how often it was generated, and which of the row's biases it has; in one
+  // word when both fit 16 bits (history and biases of at most 65535 entries)
+  unsigned* count = reinterpret_cast<unsigned*>(lsm);                                         // [kSlice]
+  unsigned* bias = reinterpret_cast<unsigned*>(lsm + (history && !a.packed ? kSlice * 4 : 0));  // [kSlice]
+  const int bias_shift = a.packed ? 16 : 0;
+  const unsigned count_mask = a.packed ? 0xffffu : 0xffffffffu;
+  __shared__ __align__(16) unsigned bits[kSlice / 32][4];  // a bit per token: seen, said, has a bias; allowed
+  constexpr int kSeen = 0, kSaid = 1, kBias = 2, kAllowed = 3;
   const int b = blockIdx.y, v0 = blockIdx.x * kSlice, tid = threadIdx.x;
   const int nv = min(kSlice, a.V - v0);
   const T* in = static_cast<const T*>(a.in) + (int64_t)b * a.in_stride + v0;
@@ -89,42 +103,36 @@ __global__ void __launch_bounds__(kLogitThreads, 3) logits_process_kernel(const 
   // rows of odd length or stride are not 16-byte aligned: those rows move element by element
   const bool wide = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
 
-  __align__(16) T x[kPer];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e0 = (j * kLogitThreads + tid) * VEC;
-    if (wide && e0 + VEC <= nv) {
-      *reinterpret_cast<uint4*>(&x[j * VEC]) = *reinterpret_cast<const uint4*>(in + e0);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (e0 + e < nv) x[j * VEC + e] = in[e0 + e];
-    }
-  }
-
+  // what is needed first is asked for first: the row's scalars, its first ids (whatever its length:
+  // the row is max_tokens wide), its mask, then the logits
   const float rep = history && a.r.repetition ? a.r.repetition[b] : 1.f;
   const float freq = history && a.r.frequency ? a.r.frequency[b] : 0.f;
   const float pres = history && a.r.presence ? a.r.presence[b] : 0.f;
   const uint32_t* mask = a.r.mask ? a.r.mask + (int64_t)b * a.r.mask_stride : nullptr;
-  unsigned allow[NV];
+  const int32_t* tok = history ? a.r.tokens + (int64_t)b * a.r.tokens_stride : nullptr;
+  const int width = history ? a.r.max_tokens : 0;
+  // ids of a thread in registers, 5120 of a row together: one round trip to memory for most rows,
+  // and the second pass over them (the counting) needs none
+  constexpr int kMany = 20;
+  unsigned t[kMany];
+  auto fetch = [&](int j0) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    // the first of VEC (4 or 8) tokens is a multiple of it: their bits lie in one word
-    const int e0 = v0 + (j * kLogitThreads + tid) * VEC;
-    allow[j] = mask && e0 < a.V ? mask[e0 >> 5] >> (e0 & 31) : 0xffffffffu;
-  }
-
-  // which tokens of the run the history and the biases name: one bit each, so that nothing else has
-  // to be cleared, and a run of logits without any is only masked and copied
+    for (int j = 0; j < kMany; ++j) {
+      const int i = j0 + j * kLogitThreads + tid;
+      t[j] = (unsigned)v0 - 1u;  // outside the run
+      if (i < width) t[j] = load_now(tok + i);
+    }
+#pragma unroll
+    for (int j = 0; j < kMany; ++j) t[j] -= (unsigned)v0;
+  };
+  fetch(0);
   bool bad = false;
   int plen = 0, len = 0, i0 = 0, i1 = 0;
-  const int32_t* tok = nullptr;
   if (history) {
     const int raw = a.r.token_lens[b], raw_p = a.r.prompt_lens ? a.r.prompt_lens[b] : 0;
     len = min(max(raw, 0), a.r.max_tokens);
     plen = min(max(raw_p, 0), len);
     bad = raw != len || raw_p < 0 || raw_p > a.r.max_tokens;
-    tok = a.r.tokens + (int64_t)b * a.r.tokens_stride;
   }
   if (biased) {
     const int raw0 = a.r.bias_offsets[b], raw1 = a.r.bias_offsets[b + 1];
@@ -132,121 +140,193 @@ __global__ void __launch_bounds__(kLogitThreads, 3) logits_process_kernel(const 
     i1 = min(max(raw1, i0), a.r.n_bias);
     bad = bad || raw0 != i0 || raw1 != i1;
   }
+  // the row's first biases
+  unsigned near_id[kNear];
+  float near_val[kNear];
+#pragma unroll
+  for (int k = 0; k < kNear; ++k) {
+    const int i = i0 + k * kLogitThreads + tid;
+    near_id[k] = (unsigned)v0 - 1u;  // outside the run
+    near_val[k] = 0.f;
+    if (i < i1) {
+      near_id[k] = load_now(a.r.bias_ids + i);
+      near_val[k] = __uint_as_float(load_now(reinterpret_cast<const int32_t*>(a.r.bias_vals + i)));
+    }
+  }
+  static_assert(kSlice / 32 == kLogitThreads, "a word of the mask per thread");
+  const int left = nv - tid * 32;
+  // tokens past the row's end are barred like masked ones
+  unsigned allowed = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0u;
+  if (mask && left > 0) allowed &= mask[(v0 >> 5) + tid];
+  const bool whole = wide && nv == kSlice;
+  __align__(16) T x[kPer];
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      *reinterpret_cast<uint4*>(&x[j * VEC]) = *reinterpret_cast<const uint4*>(in + (j * kLogitThreads + tid) * VEC);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e0 = (j * kLogitThreads + tid) * VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[j * VEC + e] = e0 + e < nv ? in[e0 + e] : from_f32<T>(0.f);
+    }
+  }
+
   if (bad && tid == 0 && blockIdx.x == 0) set_device_error(VV_ERR_RANGE);
+  // which tokens of the run the history and the biases name: one bit each, so that nothing else has
+  // to be cleared, and logits without any are only masked and copied
+  *reinterpret_cast<uint4*>(bits[tid]) = make_uint4(0, 0, 0, allowed);
+  __syncthreads();
   if (history || biased) {
-    for (int i = tid; i < 3 * kSlice / 32; i += kLogitThreads) (&bits[0][0])[i] = 0;
-    __syncthreads();
     // a prompt may hold one id thousands of times: the bit is looked at before it is set
     auto mark = [&](int which, unsigned d) {
-      volatile unsigned* word = &bits[which][d >> 5];
-      if (!((*word >> (d & 31)) & 1)) atomicOr(&bits[which][d >> 5], 1u << (d & 31));
+      volatile unsigned* word = &bits[d >> 5][which];
+      if (!((*word >> (d & 31)) & 1)) atomicOr(&bits[d >> 5][which], 1u << (d & 31));
     };
-    constexpr int kMany = 4;  // ids of a thread on their way at once
-    for (int j0 = 0; j0 < len; j0 += kMany * kLogitThreads) {
-      unsigned t[kMany];
+    constexpr int kRound = kMany * kLogitThreads;
+    for (int j0 = 0; j0 < len; j0 += kRound) {
+      if (j0 > 0) fetch(j0);
 #pragma unroll
-      for (int j = 0; j < kMany; ++j) {
-        const int i = j0 + j * kLogitThreads + tid;
-        t[j] = i < len ? (unsigned)tok[i] - (unsigned)v0 : 0xffffffffu;
-      }
+      for (int g = 0; g < kMany; g += 4) {
+        if (j0 + g * kLogitThreads >= len) break;
+        // mostly none of the four falls into the run
+        if (min(min(t[g], t[g + 1]), min(t[g + 2], t[g + 3])) >= (unsigned)nv) continue;
 #pragma unroll
-      for (int j = 0; j < kMany; ++j) {
-        if (t[j] >= (unsigned)nv) continue;
-        if (j0 + j * kLogitThreads + tid < plen) {
-          mark(kSeen, t[j]);
-        } else {
-          mark(kSaid, t[j]);
-          count[t[j]] = 0;
+        for (int j = g; j < g + 4; ++j) {
+          const int i = j0 + j * kLogitThreads + tid;
+          if (t[j] >= (unsigned)nv || i >= len) continue;
+          if (i < plen) {
+            mark(kSeen, t[j]);
+          } else {
+            mark(kSaid, t[j]);
+            count[t[j]] = 0;
+          }
         }
       }
     }
-    for (int i = i0 + tid; i < i1; i += kLogitThreads) {
-      const unsigned d = (unsigned)a.r.bias_ids[i] - (unsigned)v0;
-      if (d < (unsigned)nv) {
-        mark(kBias, d);
-        bias[d] = 0;
+    // f(entry, token of the run): the biases that fall into it
+    auto each_bias = [&](auto&& f) {
+#pragma unroll
+      for (int k = 0; k < kNear; ++k) {
+        const unsigned d = near_id[k] - (unsigned)v0;
+        if (d < (unsigned)nv) f(k * kLogitThreads + tid, d);
       }
-    }
+      for (int i = i0 + kNear * kLogitThreads + tid; i < i1; i += kLogitThreads) {
+        const unsigned d = (unsigned)a.r.bias_ids[i] - (unsigned)v0;
+        if (d < (unsigned)nv) f(i - i0, d);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kNear; ++k) bias_val[k * kLogitThreads + tid] = near_val[k];
+    each_bias([&](int, unsigned d) {
+      mark(kBias, d);
+      bias[d] = 0;
+    });
     __syncthreads();
-    for (int j0 = plen; j0 < len; j0 += kLogitThreads) {  // whole warps, for the match
-      const int i = j0 + tid;
-      unsigned d = i < len ? (unsigned)tok[i] - (unsigned)v0 : 0xffffffffu;
-      if (d >= (unsigned)nv) d = 0xffffffffu;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (d != 0xffffffffu && (tid & 31) == __ffs(same) - 1) atomicAdd(&count[d], __popc(same));
-    }
     // an id named twice keeps its last value: the entry of the largest index wins
-    for (int i = i0 + tid; i < i1; i += kLogitThreads) {
-      const unsigned d = (unsigned)a.r.bias_ids[i] - (unsigned)v0;
-      if (d < (unsigned)nv) atomicMax(&bias[d], (unsigned)i);
+    each_bias([&](int k, unsigned d) { atomicMax(&bias[d], (unsigned)k << bias_shift); });
+    if (bias_shift) __syncthreads();
+    for (int j0 = plen / kRound * kRound; j0 < len; j0 += kRound) {
+      if (len > kRound) fetch(j0);
+#pragma unroll
+      for (int j = 0; j < kMany; ++j) {
+        if (j0 + (j + 1) * kLogitThreads <= plen || j0 + j * kLogitThreads >= len) continue;  // the prompt's, or none
+        const int i = j0 + j * kLogitThreads + tid;
+        const unsigned d = t[j] < (unsigned)nv && i >= plen && i < len ? t[j] : 0xffffffffu;
+        if (!__any_sync(0xffffffffu, d != 0xffffffffu)) continue;
+        const unsigned same = __match_any_sync(0xffffffffu, d);
+        if (d != 0xffffffffu && (tid & 31) == __ffs(same) - 1) atomicAdd(&count[d], __popc(same));
+      }
     }
     __syncthreads();
   }
 
-  unsigned long long best = 0;
+  // All logits: copied, barred ones as -inf.  The best of those without a rule of their own: strictly
+  // larger only, so the lowest token of equals (a thread's tokens ascend).
+  float best = -INFINITY;
+  int best_at = 0;
+  constexpr unsigned kAll = (1u << VEC) - 1;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e0 = (j * kLogitThreads + tid) * VEC;
-    if (e0 >= nv) continue;
-    const unsigned allowed = allow[j];
-    unsigned seen = 0, said = 0, named = 0;
-    if (history || biased) {
-      seen = bits[kSeen][e0 >> 5] >> (e0 & 31);
-      said = bits[kSaid][e0 >> 5] >> (e0 & 31);
-      named = bits[kBias][e0 >> 5] >> (e0 & 31);
-    }
-    const bool any = ((seen | said | named) & ((1u << VEC) - 1)) != 0;
+    const int e0 = (j * kLogitThreads + tid) * VEC;  // its VEC (4 or 8) bits lie in one word
+    const uint4 word = *reinterpret_cast<const uint4*>(bits[e0 >> 5]);
+    const unsigned named = (word.x | word.y | word.z) >> (e0 & 31), barred = ~(word.w >> (e0 & 31));
+    float y[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int i = e0 + e;
-      if (i >= nv) break;
-      float y = to_f32<T>(x[j * VEC + e]);
-      if (any) {
-        if (((seen | said) >> e) & 1) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
-        if ((said >> e) & 1) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)count[i])), pres);
-        if ((named >> e) & 1) y = __fadd_rn(y, a.r.bias_vals[bias[i]]);
-      }
-      if (!((allowed >> e) & 1)) y = -INFINITY;
-      x[j * VEC + e] = from_f32<T>(y);
-      if (y > -INFINITY) {
-        const unsigned long long key = ((unsigned long long)ordered_bits(y) << 32) | (0xffffffffu - (unsigned)(v0 + i));
-        best = key > best ? key : best;
+    for (int e = 0; e < VEC; ++e) y[e] = to_f32<T>(x[j * VEC + e]);
+    if ((named | barred) & kAll) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        if ((barred >> e) & 1) x[j * VEC + e] = from_f32<T>(-INFINITY);
+        if (((named | barred) >> e) & 1) y[e] = -INFINITY;
       }
     }
-    if (wide && e0 + VEC <= nv) {
+    if (whole) {
       *reinterpret_cast<uint4*>(out + e0) = *reinterpret_cast<const uint4*>(&x[j * VEC]);
     } else {
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
         if (e0 + e < nv) out[e0 + e] = x[j * VEC + e];
     }
+    float top = y[0];
+#pragma unroll
+    for (int e = 1; e < VEC; ++e) top = fmaxf(top, y[e]);  // NaN only where all are
+    if (top > best) {
+      best = top;
+#pragma unroll
+      for (int e = VEC - 1; e >= 0; --e)
+        if (y[e] == top) best_at = v0 + e0 + e;
+    }
+  }
+  // The few that the history or a bias names, a word of 32 tokens per thread; their logits stand
+  // unchanged where they were read (in place: as the copy just written).
+  if (history || biased) {
+    __syncthreads();
+    const uint4 word = *reinterpret_cast<const uint4*>(bits[tid]);
+    for (unsigned rest = (word.x | word.y | word.z) & word.w; rest; rest &= rest - 1) {
+      const unsigned bit = rest & -rest;
+      const int d = tid * 32 + __ffs(rest) - 1;
+      float y = to_f32<T>(in[d]);
+      if ((word.x | word.y) & bit) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+      if (word.y & bit) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)(count[d] & count_mask))), pres);
+      if (word.z & bit) {
+        const unsigned k = bias[d] >> bias_shift;
+        y = __fadd_rn(y, k < kNear * kLogitThreads ? bias_val[k] : a.r.bias_vals[i0 + k]);
+      }
+      out[d] = from_f32<T>(y);
+      if (y > best || (y == best && v0 + d < best_at)) {
+        best = y;
+        best_at = v0 + d;
+      }
+    }
   }
   if (!a.argmax) return;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
-    best = other > best ? other : best;
-  }
-  if ((tid & 31) == 0) warp_key[tid >> 5] = best;
+  // the warp's best: the largest value, then the lowest of its tokens
+  const unsigned mine = best > -INFINITY ? ordered_bits(best) : 0u;
+  const unsigned top = __reduce_max_sync(0xffffffffu, mine);
+  const unsigned at = __reduce_min_sync(0xffffffffu, mine == top ? (unsigned)best_at : 0xffffffffu);
+  unsigned long long key = top ? ((unsigned long long)top << 32) | (0xffffffffu - at) : 0ull;
+  if ((tid & 31) == 0) warp_key[tid >> 5] = key;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < kLogitThreads / 32; ++w) best = warp_key[w] > best ? warp_key[w] : best;
+    for (int w = 1; w < kLogitThreads / 32; ++w) key = warp_key[w] > key ? warp_key[w] : key;
     RowBest* row = a.ws + b;
     if (gridDim.x > 1) {
-      if (best) atomicMax(&row->key, best);
+      if (key) atomicMax(&row->key, key);
       __threadfence();
       if (atomicAdd(&row->arrived, 1u) != gridDim.x - 1) return;
       __threadfence();
-      best = atomicExch(&row->key, 0ull);
+      key = atomicExch(&row->key, 0ull);
       row->arrived = 0;
     }
-    a.argmax[b] = best ? (int)(0xffffffffu - (unsigned)best) : -1;
+    a.argmax[b] = key ? (int)(0xffffffffu - (unsigned)key) : -1;
   }
 }
 
 template <typename T>
 cudaError_t launch_logits(const LogitsArgs& a, int B, cudaStream_t s) {
-  const size_t smem = (a.r.tokens ? kSlice * 4 : 0) + (a.r.bias_ids ? kSlice * 4 : 0);
+  const size_t smem = (a.r.tokens ? kSlice * 4 : 0) + (a.r.bias_ids && !a.packed ? kSlice * 4 : 0);
   cudaError_t e = cudaFuncSetAttribute(logits_process_kernel<T>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSlice * 8);
   if (e != cudaSuccess) return e;
@@ -312,7 +392,7 @@ extern "C" vv_status vv_logits_process(const void* logits, int64_t logits_stride
   a.argmax = argmax;
   a.ws = static_cast<vv::RowBest*>(ws);
   a.V = (int)V;
-  a.words = words;
+  a.packed = r.tokens && r.bias_ids && r.max_tokens < 65536 && r.n_bias < 65536;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = dtype == VV_F32   ? vv::launch_logits<float>(a, B, s)
                   : dtype == VV_F16 ? vv::launch_logits<__half>(a, B, s)

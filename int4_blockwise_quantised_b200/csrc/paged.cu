@@ -311,18 +311,6 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) qk_rope_append_kernel(cons
 
   const int c = lane & 15;  // 16-byte piece of the row
   const float sign = c < 8 ? -1.f : 1.f;
-  uint32_t qg[4], qo[4], kg[4], ko[4];  // gains of this piece and of its partner
-  if (GAINS) {
-    const uint32_t one = pack2<T>(1.f, 1.f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t *gq = static_cast<const uint32_t*>(a.q_gain), *gk = static_cast<const uint32_t*>(a.k_gain);
-      qg[j] = gq ? gq[c * 4 + j] : one;
-      qo[j] = gq ? gq[(c ^ 8) * 4 + j] : one;
-      kg[j] = gk ? gk[c * 4 + j] : one;
-      ko[j] = gk ? gk[(c ^ 8) * 4 + j] : one;
-    }
-  }
   const double f0 = a.turns[lane], f1 = a.turns[lane + 32];
   int pos = 0;
   int64_t slot = -1;
@@ -354,59 +342,66 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) qk_rope_append_kernel(cons
       slot = a.slots[(u + step) / a.parts];
     }
     __syncwarp();
-    float2 w[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const float4 f = *reinterpret_cast<const float4*>(&cs[(c & 7) * 8 + j]);
-      w[j] = make_float2(f.x, f.y * sign);
-      w[j + 1] = make_float2(f.z, f.w * sign);
-    }
-    wait_phase(&full[st], round & 1);
-    const unsigned char* in = ring + st * unit_bytes;
-#pragma unroll 2
-    for (int r = lane >> 4; r < ((nh + 1) & ~1); r += 2) {
-      const bool live = r < nh;
-      const int head = h0 + r;
-      const bool is_q = head < a.Hq, is_k = !is_q && head < a.Hq + a.Hkv;
-      uint4 own = make_uint4(0, 0, 0, 0), par = own;
-      if (live) {
-        own = *reinterpret_cast<const uint4*>(in + r * kRow + c * 16);
-        par = *reinterpret_cast<const uint4*>(in + r * kRow + (c ^ 8) * 16);
-      }
-      const uint32_t ow[4] = {own.x, own.y, own.z, own.w}, pw[4] = {par.x, par.y, par.z, par.w};
-      float x[8], y[8];
+    // y = x * own + partner * other, pairs of elements: the cosines and sines times the gains
+    float2 own[4], other[4];
+    auto factors = [&](const void* gain) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack2<T>(ow[j]), g = unpack2<T>(pw[j]);
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
-        y[2 * j] = g.x;
-        y[2 * j + 1] = g.y;
-      }
-      if (GAINS) {
-        float ss = 0.f, inv = 1.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (is_q ? a.q_gain != nullptr : a.k_gain != nullptr) inv = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = unpack2<T>(is_q ? qg[j] : kg[j]), g = unpack2<T>(is_q ? qo[j] : ko[j]);
-          x[2 * j] *= inv * f.x;
-          x[2 * j + 1] *= inv * f.y;
-          y[2 * j] *= inv * g.x;
-          y[2 * j + 1] *= inv * g.y;
+        const float4 f = *reinterpret_cast<const float4*>(&cs[(c & 7) * 8 + 2 * j]);
+        own[j] = make_float2(f.x, f.z);
+        other[j] = make_float2(f.y * sign, f.w * sign);
+        if (GAINS && gain) {
+          const float2 g = unpack2<T>(static_cast<const uint32_t*>(gain)[c * 4 + j]);
+          const float2 h = unpack2<T>(static_cast<const uint32_t*>(gain)[(c ^ 8) * 4 + j]);
+          own[j] = make_float2(own[j].x * g.x, own[j].y * g.y);
+          other[j] = make_float2(other[j].x * h.x, other[j].y * h.y);
         }
       }
+    };
+    // rows from .. to - 1 of the unit, two at a time, row r to dst + r * pitch
+    auto turn = [&](int from, int to, bool norm, char* dst, int64_t pitch) {
+      const unsigned char* in = ring + st * unit_bytes + c * 16;
+      const int swap = (c < 8 ? 8 : -8) * 16;
+#pragma unroll 4
+      for (int r0 = from; r0 < to; r0 += 2) {
+        const int r = min(r0 + (lane >> 4), to - 1);  // an odd last row is done twice
+        const uint4 xw = *reinterpret_cast<const uint4*>(in + r * kRow);
+        const uint4 pw = *reinterpret_cast<const uint4*>(in + r * kRow + swap);
+        float2 x[4] = {unpack2<T>(xw.x), unpack2<T>(xw.y), unpack2<T>(xw.z), unpack2<T>(xw.w)};
+        const float2 p[4] = {unpack2<T>(pw.x), unpack2<T>(pw.y), unpack2<T>(pw.z), unpack2<T>(pw.w)};
+        float inv = 1.f;
+        if (GAINS && norm) {
+          float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], w[j].x, y[j] * w[j].y);
-      uint4 out = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
-      if (!is_q && !is_k) out = own;
-      char* dst = is_q ? a.q_out + t * a.qo_stride + head * kRow
-                       : is_k ? a.kp + at + (head - a.Hq) * a.head_stride
-                              : a.vp + at + (head - a.Hq - a.Hkv) * a.head_stride;
-      if (live && (is_q || at >= 0)) *reinterpret_cast<uint4*>(dst + c * 16) = out;
+          for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(x[j], x[j], s2);
+          float ss = s2.x + s2.y;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          inv = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
+        }
+        const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] = __ffma2_rn(x[j], own[j], __fmul2_rn(p[j], other[j]));
+          if (GAINS) x[j] = __fmul2_rn(x[j], inv2);
+        }
+        *reinterpret_cast<uint4*>(dst + r * pitch) = make_uint4(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y),
+                                                                pack2<T>(x[2].x, x[2].y), pack2<T>(x[3].x, x[3].y));
+      }
+    };
+    const int q_end = min(max(a.Hq - h0, 0), nh), k_end = min(max(a.Hq + a.Hkv - h0, 0), nh);
+    if (q_end > 0 || (k_end > 0 && at >= 0)) factors(q_end > 0 ? a.q_gain : a.k_gain);
+    wait_phase(&full[st], round & 1);
+    if (q_end > 0) turn(0, q_end, a.q_gain != nullptr, a.q_out + t * a.qo_stride + h0 * kRow + c * 16, kRow);
+    if (at >= 0) {
+      if (k_end > q_end) {
+        if (GAINS && q_end > 0) factors(a.k_gain);
+        turn(q_end, k_end, a.k_gain != nullptr, a.kp + at + (h0 - a.Hq) * a.head_stride + c * 16, a.head_stride);
+      }
+#pragma unroll 2
+      for (int r = k_end + (lane >> 4); r < nh; r += 2)
+        *reinterpret_cast<uint4*>(a.vp + at + (h0 + r - a.Hq - a.Hkv) * a.head_stride + c * 16) =
+            *reinterpret_cast<const uint4*>(ring + st * unit_bytes + r * kRow + c * 16);
     }
     __syncwarp();
     copy(u + kRopeStages * step, st);

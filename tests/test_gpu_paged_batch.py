@@ -500,7 +500,8 @@ def logits_check(c, out, idx):
 
 LOGITS = [(1, 1, 0, F32, 0, False), (1, 1000, 5, F32, 0, False), (2, 1001, 100, F32, 9, True),
           (3, 8192, 64, BF16, 0, True), (5, 8193, 700, F16, 30, True), (2, 151936, 300, F32, 40, False),
-          (7, 33001, 0, F32, 12, True), (65, 2049, 33, BF16, 3, False), (4, 20000, 3000, F32, 500, True)]
+          (7, 33001, 0, F32, 12, True), (65, 2049, 33, BF16, 3, False), (4, 20000, 3000, F32, 500, True),
+          (2, 9001, 70000, F32, 2000, True), (2, 300, 6000, F16, 70000, False)]
 
 
 @pytest.mark.parametrize("B,V,W,dtype,bias,mask", LOGITS)
