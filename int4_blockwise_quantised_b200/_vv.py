@@ -6,7 +6,6 @@ there is no fallback of any kind, and importing this module fails loudly when li
 been built.
 """
 
-import contextlib
 import ctypes
 import os
 import re
@@ -147,6 +146,12 @@ def _load():
 
 
 lib = _load()
+try:
+    from . import _marshal
+except ImportError as e:
+    raise ImportError("_marshal.so is missing or does not load: build it with `python -m "
+                      "int4_blockwise_quantised_b200.build`") from e
+_marshal.set_error(VVError)
 
 
 def header_functions(path=HEADER_PATH):
@@ -276,60 +281,18 @@ def vv_lm_head_argmax(x, gamma, w_lm, eps, ws, logits=True, stream=None):
 # These entry points take tensors of any device (all of one call on the same one): the call runs
 # with that device current, on `stream` or on the device's current torch stream, and the tensors it
 # makes are made on that stream.  A tensor of the wrong type, shape, layout or device is a VVError
-# (VV_ERR_INVALID_ARG), raised before anything is launched.
+# (VV_ERR_INVALID_ARG), raised before anything is launched.  The arguments are looked at and turned
+# into pointers by the extension module _marshal.
+def _on(stream, function, *args):
+    """function(*args) with `stream` (a torch.cuda.Stream) and its device current."""
+    if stream.device != args[0].device:
+        raise VVError(VV_ERR_INVALID_ARG, f"stream of {stream.device}, tensors on {args[0].device}")
+    with torch.cuda.stream(stream):
+        return function(*args)
+
+
 def _refuse(text):
     raise VVError(VV_ERR_INVALID_ARG, text)
-
-
-def _same(device, who, **tensors):
-    """Every given tensor lives on `device` (a CUDA one)."""
-    if device.type != "cuda":
-        _refuse(f"{who}: tensors must be on a CUDA device, got {device}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            _refuse(f"{who}: {name} is on {t.device}, expected {device}")
-
-
-def _dense(who, dtype, **tensors):
-    """Every given (name=(tensor, shape)) is contiguous, of `dtype` and `shape` (None: any)."""
-    for name, (t, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != dtype or not t.is_contiguous():
-            _refuse(f"{who}: {name} must be contiguous {dtype}, got {t.dtype}, strides {t.stride()}")
-        if shape is not None and tuple(t.shape) != shape:
-            _refuse(f"{who}: {name} has shape {tuple(t.shape)}, expected {shape}")
-
-
-def _rows(who, name, t, dtype, last):
-    """`t` is [rows, ...] of `dtype` whose trailing dimensions `last` are contiguous in a row;
-    returns the row stride in elements."""
-    if t.dtype != dtype:
-        _refuse(f"{who}: {name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 + len(last) or tuple(t.shape[1:]) != last:
-        _refuse(f"{who}: {name} has shape {tuple(t.shape)}, expected [rows, {', '.join(map(str, last))}]")
-    want = 1
-    for size, stride in zip(reversed(last), reversed(t.stride()[1:])):
-        if size > 1 and stride != want:
-            _refuse(f"{who}: the rows of {name} must be contiguous, strides {t.stride()}")
-        want *= size
-    return t.stride(0) if t.shape[0] > 1 else want
-
-
-@contextlib.contextmanager
-def _switched(device, stream):
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield
-
-
-_here = contextlib.nullcontext()
-
-
-def _on(device, stream):
-    """Context in which `device` and `stream` (None: its current one) are current."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return _here
-    return _switched(device, stream)
 
 
 class PagedKV:
@@ -345,16 +308,18 @@ class PagedKV:
             _refuse(f"PagedKV: fp16 or bf16 pages, got {k.dtype}")
         if k.stride(3) != 1 and k.shape[3] > 1:
             _refuse("PagedKV: the last dimension must be contiguous")
-        _same(k.device, "PagedKV", v=v)
+        if not k.is_cuda or v.device != k.device:
+            _refuse(f"PagedKV: k and v must be on one CUDA device, got {k.device} and {v.device}")
         self.k, self.v = k, v
         self.pages, self.heads, self.page_size, self.head_dim = k.shape
         self.dtype, self.device = k.dtype, k.device
         self.c = vv_paged_kv(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
                              self.pages, self.page_size, DTYPES[k.dtype])
-        self.ref = ctypes.byref(self.c)
+        self._call = (ctypes.addressof(self.c), self.heads, self.head_dim, k.get_device())
 
 
 PagedPlan = namedtuple("PagedPlan", "lens offsets slots positions cursor")
+_NO_PLAN = (None,) * 5
 
 
 def vv_paged_plan(lens, new_lens, block_tables, free_pages, page_size, pages, max_tokens,
@@ -365,36 +330,10 @@ def vv_paged_plan(lens, new_lens, block_tables, free_pages, page_size, pages, ma
     int32 [n] of page numbers in [0, pages), taken from index *cursor (int32 [1], None: 0) on.
     Returns PagedPlan(lens int32 [B], offsets int32 [B + 1], slots int64 [max_tokens], positions
     int32 [max_tokens], cursor int32 [1]); `out` may give such a tuple to write into."""
-    who, dev, B = "vv_paged_plan", lens.device, lens.numel()
-    _same(dev, who, new_lens=new_lens, block_tables=block_tables, free_pages=free_pages,
-          cursor=cursor)
-    if block_tables.dim() != 2:
-        _refuse(f"{who}: block_tables must be [B, max_blocks]")
-    _dense(who, torch.int32, lens=(lens, (B,)), new_lens=(new_lens, (B,)),
-           block_tables=(block_tables, (B, block_tables.shape[1])),
-           free_pages=(free_pages, (free_pages.numel(),)), cursor=(cursor, (1,)))
-    with _on(dev, stream):
-        if out is None:
-            e = torch.empty
-            out = PagedPlan(e(B, dtype=torch.int32, device=dev),
-                            e(B + 1, dtype=torch.int32, device=dev),
-                            e(max_tokens, dtype=torch.int64, device=dev),
-                            e(max_tokens, dtype=torch.int32, device=dev),
-                            e(1, dtype=torch.int32, device=dev))
-        else:
-            out = PagedPlan(*out)
-            _same(dev, who, **out._asdict())
-            _dense(who, torch.int32, lens=(out.lens, (B,)), offsets=(out.offsets, (B + 1,)),
-                   positions=(out.positions, (max_tokens,)), cursor=(out.cursor, (1,)))
-            _dense(who, torch.int64, slots=(out.slots, (max_tokens,)))
-        check(lib.vv_paged_plan(lens.data_ptr(), new_lens.data_ptr(), B, prefix_len, page_size,
-                                pages, free_pages.data_ptr(), free_pages.numel(),
-                                None if cursor is None else cursor.data_ptr(),
-                                block_tables.data_ptr(), block_tables.shape[1],
-                                out.lens.data_ptr(), out.offsets.data_ptr(), out.slots.data_ptr(),
-                                out.positions.data_ptr(), max_tokens, out.cursor.data_ptr(),
-                                stream_handle(stream)))
-    return out
+    args = (lens, new_lens, block_tables, free_pages, page_size, pages, max_tokens, prefix_len,
+            cursor, *(out or _NO_PLAN))
+    r = _marshal.paged_plan(*args) if stream is None else _on(stream, _marshal.paged_plan, *args)
+    return PagedPlan(*r)
 
 
 def vv_qk_rope_append(q, k, v, positions, slots, kv, theta, q_gain=None, k_gain=None, eps=1e-6,
@@ -404,30 +343,10 @@ def vv_qk_rope_append(q, k, v, positions, slots, kv, theta, q_gain=None, k_gain=
 
     q [T, Hq, 128], k, v [T, Hkv, 128] of the pool's type, rows may be strided; positions int32
     [T]; slots int64 [T]; gains [128].  out: [T, Hq, 128], q itself allowed."""
-    who, dev, dt = "vv_qk_rope_append", q.device, kv.dtype
-    T, Hq, D = q.shape if q.dim() == 3 else _refuse(f"{who}: q must be [T, Hq, D]")
-    _same(dev, who, k=k, v=v, positions=positions, slots=slots, kv=kv, q_gain=q_gain,
-          k_gain=k_gain, out=out)
-    tail = (kv.heads, kv.head_dim)
-    if D != kv.head_dim or k.shape[0] != T or v.shape[0] != T:
-        _refuse(f"{who}: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, head dimension "
-                f"{kv.head_dim}")
-    qs, ks, vs = (_rows(who, "q", q, dt, (Hq, D)), _rows(who, "k", k, dt, tail),
-                  _rows(who, "v", v, dt, tail))
-    _dense(who, torch.int32, positions=(positions, (T,)))
-    _dense(who, torch.int64, slots=(slots, (T,)))
-    _dense(who, dt, q_gain=(q_gain, (D,)), k_gain=(k_gain, (D,)))
-    with _on(dev, stream):
-        o = out if out is not None else torch.empty((T, Hq, D), dtype=dt, device=dev)
-        os = _rows(who, "out", o, dt, (Hq, D))
-        if o.shape[0] != T:
-            _refuse(f"{who}: out has {o.shape[0]} rows, expected {T}")
-        check(lib.vv_qk_rope_append(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq,
-                                    kv.heads, D, None if q_gain is None else q_gain.data_ptr(),
-                                    None if k_gain is None else k_gain.data_ptr(), eps,
-                                    positions.data_ptr(), theta, slots.data_ptr(), kv.ref,
-                                    o.data_ptr(), os, stream_handle(stream)))
-    return o
+    args = (q, k, v, positions, slots, *kv._call, theta, q_gain, k_gain, eps, out)
+    if stream is None:
+        return _marshal.qk_rope_append(*args)
+    return _on(stream, _marshal.qk_rope_append, *args)
 
 
 def vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, D, prefix_len, max_own):
@@ -442,44 +361,10 @@ def vv_gqa_prefix_attn(q, k_prefix, v_prefix, kv, block_tables, lens, scale, ws,
     block_tables int32 [B, max_blocks]; lens int32 [B] (tokens in the pages; < 0: padding row);
     ws: zero-filled once, vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, 128, P, max_blocks *
     page_size) bytes.  Returns out [B, Hq, 128]; lse fp32 [B, Hq] receives the log sums."""
-    who, dev, dt = "vv_gqa_prefix_attn", q.device, kv.dtype
-    B, Hq, D = q.shape if q.dim() == 3 else _refuse(f"{who}: q must be [B, Hq, D]")
-    _same(dev, who, k_prefix=k_prefix, v_prefix=v_prefix, kv=kv, block_tables=block_tables,
-          lens=lens, ws=ws, out=out, lse=lse)
-    if D != kv.head_dim:
-        _refuse(f"{who}: q {tuple(q.shape)}, head dimension {kv.head_dim}")
-    if (k_prefix is None) != (v_prefix is None):
-        _refuse(f"{who}: k_prefix and v_prefix go together")
-    P, ph, pt, kp, vp = 0, 0, 0, None, None
-    if k_prefix is not None:
-        if (k_prefix.dim() != 3 or k_prefix.shape[0] != kv.heads or k_prefix.shape[2] != D or
-                v_prefix.shape != k_prefix.shape or v_prefix.stride() != k_prefix.stride() or
-                k_prefix.dtype != dt or v_prefix.dtype != dt or k_prefix.stride(2) != 1):
-            _refuse(f"{who}: k_prefix and v_prefix must be {dt} [{kv.heads}, P, {D}] of one layout, "
-                    "the last dimension contiguous")
-        P, ph, pt = k_prefix.shape[1], k_prefix.stride(0), k_prefix.stride(1)
-        if P < 2:
-            pt = max(pt, D)
-        kp, vp = k_prefix.data_ptr(), v_prefix.data_ptr()
-    if block_tables.dim() != 2:
-        _refuse(f"{who}: block_tables must be [B, max_blocks]")
-    blocks = block_tables.shape[1]
-    _dense(who, torch.int32, block_tables=(block_tables, (B, blocks)), lens=(lens, (B,)))
-    _dense(who, torch.float32, lse=(lse, (B, Hq)))
-    if not ws.is_contiguous():
-        _refuse(f"{who}: ws must be contiguous")
-    qs = _rows(who, "q", q, dt, (Hq, D))
-    with _on(dev, stream):
-        o = out if out is not None else torch.empty((B, Hq, D), dtype=dt, device=dev)
-        os = _rows(who, "out", o, dt, (Hq, D))
-        if o.shape[0] != B:
-            _refuse(f"{who}: out has {o.shape[0]} rows, expected {B}")
-        check(lib.vv_gqa_prefix_attn(q.data_ptr(), qs, B, Hq, kv.heads, D, kp, vp, ph, pt, P,
-                                     kv.ref, block_tables.data_ptr(), blocks, lens.data_ptr(),
-                                     scale, o.data_ptr(), os,
-                                     None if lse is None else lse.data_ptr(), ws.data_ptr(),
-                                     ws.numel() * ws.element_size(), stream_handle(stream)))
-    return o
+    args = (q, k_prefix, v_prefix, *kv._call, block_tables, lens, scale, ws, out, lse)
+    if stream is None:
+        return _marshal.gqa_prefix_attn(*args)
+    return _on(stream, _marshal.gqa_prefix_attn, *args)
 
 
 def vv_logits_process_workspace_size(B):
@@ -498,53 +383,8 @@ def vv_logits_process(logits, ws=None, tokens=None, token_lens=None, prompt_lens
     int32 [B + 1]; mask int32 [B, ceil(V / 32)], bit v % 32 of word v / 32 set = allowed.
     ws (needed with argmax): zero-filled once, vv_logits_process_workspace_size(B) bytes.  out may
     be logits itself."""
-    who, dev = "vv_logits_process", logits.device
-    if logits.dim() != 2 or logits.dtype not in DTYPES:
-        _refuse(f"{who}: logits must be fp32, fp16 or bf16 [B, V]")
-    B, V = logits.shape
-    _same(dev, who, ws=ws, tokens=tokens, token_lens=token_lens, prompt_lens=prompt_lens,
-          repetition=repetition, frequency=frequency, presence=presence, bias_ids=bias_ids,
-          bias_vals=bias_vals, bias_offsets=bias_offsets, mask=mask, out=out)
-    _dense(who, torch.int32, token_lens=(token_lens, (B,)), prompt_lens=(prompt_lens, (B,)),
-           bias_ids=(bias_ids, None), bias_offsets=(bias_offsets, (B + 1,)))
-    _dense(who, torch.float32, repetition=(repetition, (B,)), frequency=(frequency, (B,)),
-           presence=(presence, (B,)), bias_vals=(bias_vals, None))
-    r = vv_logits_rules()
-    if tokens is not None:
-        if token_lens is None or tokens.dim() != 2 or tokens.shape[0] != B:
-            _refuse(f"{who}: tokens must be [B, width] and come with token_lens")
-        r.tokens, r.max_tokens = tokens.data_ptr(), tokens.shape[1]
-        r.tokens_stride = _rows(who, "tokens", tokens, torch.int32, (tokens.shape[1],))
-        r.token_lens = token_lens.data_ptr()
-        for name, t in (("prompt_lens", prompt_lens), ("repetition", repetition),
-                        ("frequency", frequency), ("presence", presence)):
-            if t is not None:
-                setattr(r, name, t.data_ptr())
-    elif not (repetition is None and frequency is None and presence is None):
-        _refuse(f"{who}: penalties need tokens")
-    if bias_ids is not None:
-        if bias_vals is None or bias_offsets is None or bias_vals.numel() != bias_ids.numel():
-            _refuse(f"{who}: bias_ids, bias_vals and bias_offsets go together")
-        r.bias_ids, r.bias_vals = bias_ids.data_ptr(), bias_vals.data_ptr()
-        r.bias_offsets, r.n_bias = bias_offsets.data_ptr(), bias_ids.numel()
-    if mask is not None:
-        r.mask_stride = _rows(who, "mask", mask, torch.int32, ((V + 31) // 32,))
-        if mask.shape[0] != B:
-            _refuse(f"{who}: mask has {mask.shape[0]} rows, expected {B}")
-        r.mask = mask.data_ptr()
-    ls = _rows(who, "logits", logits, logits.dtype, (V,))
-    with _on(dev, stream):
-        o = out if out is not None else torch.empty((B, V), dtype=logits.dtype, device=dev)
-        os = _rows(who, "out", o, logits.dtype, (V,))
-        if o.shape[0] != B:
-            _refuse(f"{who}: out has {o.shape[0]} rows, expected {B}")
-        idx = torch.empty(B, dtype=torch.int32, device=dev) if argmax else None
-        if argmax and (ws is None or not ws.is_contiguous()):
-            _refuse(f"{who}: argmax needs a contiguous workspace")
-        check(lib.vv_logits_process(logits.data_ptr(), ls, DTYPES[logits.dtype], B, V,
-                                    ctypes.byref(r), o.data_ptr(), os,
-                                    idx.data_ptr() if argmax else None,
-                                    ws.data_ptr() if argmax else None,
-                                    ws.numel() * ws.element_size() if argmax else 0,
-                                    stream_handle(stream)))
-    return o, idx
+    args = (logits, ws, tokens, token_lens, prompt_lens, repetition, frequency, presence, bias_ids,
+            bias_vals, bias_offsets, mask, argmax, out)
+    if stream is None:
+        return _marshal.logits_process(*args)
+    return _on(stream, _marshal.logits_process, *args)

@@ -4,7 +4,8 @@
 
 Each csrc/*.cu compiles to an object under _build/ (in parallel, skipped when up to date), then
 all objects link into int4_blockwise_quantised_b200/libvv.so with the CUDA runtime linked
-statically.
+statically.  csrc/marshal.cpp (tensor arguments of the batch operators) compiles with the host
+compiler against torch into the extension module _marshal.so, which links libvv.so.
 """
 
 import argparse
@@ -19,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvv.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -54,11 +56,41 @@ def _compile(src, force, extra):
     return obj, r.stderr
 
 
+def _compile_marshal(force):
+    src, obj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.o")
+    newest_dep = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "vv.h")))
+    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= newest_dep:
+        return obj
+    import sysconfig
+
+    from torch.utils import cpp_extension as ext
+
+    inc = ext.include_paths() + [sysconfig.get_paths()["include"], "/usr/local/cuda/include"]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-c", src, "-o", obj]
+    cmd += [f for d in inc for f in ("-isystem", d)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_marshal(obj):
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-shared", "-o", MARSHAL, obj, "-L", PKG, "-l:libvv.so", "-L", lib, "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+
+
 def build(force=False, jobs=None, verbose=False, extra=()):
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
-    with cf.ThreadPoolExecutor(jobs) as ex:
+    with cf.ThreadPoolExecutor(jobs + 1) as ex:
+        marshal = ex.submit(_compile_marshal, force)
         results = list(ex.map(lambda s: _compile(s, force, list(extra)), srcs))
     objs = [o for o, _ in results]
     if verbose:
@@ -71,6 +103,10 @@ def build(force=False, jobs=None, verbose=False, extra=()):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    obj = marshal.result()
+    if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < max(
+            os.path.getmtime(obj), os.path.getmtime(LIB)):
+        _link_marshal(obj)
     return LIB
 
 
