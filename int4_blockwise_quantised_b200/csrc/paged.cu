@@ -249,16 +249,23 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 //
 // Bound by HBM: every head row is read once and written once (512 bytes for 128 elements, about
 // 40 instructions per 32 bytes).  A unit is one token's heads, or a part of them; a warp works alone
-// on its units and has the next two on their way (cp.async.bulk into a ring of its own, a token's
-// heads of one kind are contiguous): about 150 KB per SM with 16 warps, whatever their registers,
-// and no barrier between warps.  Half a warp turns one head row, 16 bytes a lane; the rotation's
+// on its units and has the next one or two on their way (cp.async.bulk into a ring of its own, a
+// token's heads of one kind are contiguous), whatever its registers and without a barrier between
+// warps.  Half a warp turns one head row, 16 bytes a lane; the rotation's
 // partner is read from shared memory too.  A token's angles are found once per unit, two a lane: the
 // turns pos * theta^(-2i/128) / 2 pi reduced to [-1/2, 1/2] in 64 bits (in 32 bits a position of
 // 10^6 would lose the angle's second digit), then sine and cosine of the remainder in 32 bits.
 constexpr int kHeadDim = 128;
-constexpr int kRopeWarps = 8;
-constexpr int kRopeStages = 3;
-constexpr int kRopeHeads = 18;  // most heads of a unit: 8 warps x 3 x 4.5 KB, two CTAs per SM
+constexpr int kRopeHeads = 18;  // most heads of a unit, 4.5 KB
+// With norms a row takes twice the instructions: eight warps per CTA (two CTAs per SM) and one unit on
+// its way beside the one in work.  Without, as many warps ask memory for more than it gives in
+// good order: 50001 tokens of 28 + 4 + 4 heads take 172 us with eight and 156 with six (150 with
+// the slower loop that handled all rows alike); with norms 181 and 208.
+template <bool GAINS>
+struct RopeShape {
+  static constexpr int kWarps = GAINS ? 8 : 6;
+  static constexpr int kStages = GAINS ? 2 : 3;
+};
 
 struct RopeArgs {
   const char* q;
@@ -304,11 +311,12 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
 }
 
 template <typename T, bool GAINS>
-__global__ void __launch_bounds__(kRopeWarps * 32, 2) qk_rope_append_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(RopeShape<GAINS>::kWarps * 32, 2)
+    qk_rope_append_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kRow = kHeadDim * 2, kRopeWarps = RopeShape<GAINS>::kWarps, kRopeStages = RopeShape<GAINS>::kStages;
   extern __shared__ __align__(128) unsigned char ring_all[];
   __shared__ __align__(8) uint64_t full_all[kRopeWarps][kRopeStages];
   __shared__ __align__(16) float2 cs_all[kRopeWarps][kHeadDim / 2];
-  constexpr int kRow = kHeadDim * 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_heads = a.Hq + 2 * a.Hkv, unit_bytes = a.heads * kRow;
   unsigned char* ring = ring_all + warp * (kRopeStages * unit_bytes);
@@ -353,11 +361,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) qk_rope_append_kernel(cons
     const int t = (int)(u / a.parts), h0 = (int)(u - (int64_t)t * a.parts) * a.heads, nh = min(a.heads, n_heads - h0);
     {
       const double x0 = (double)pos * f0, x1 = (double)pos * f1;
-      float sn, cn;
-      sincospif(2.f * (float)(x0 - rint(x0)), &sn, &cn);
-      cs[lane] = make_float2(cn, sn);
-      sincospif(2.f * (float)(x1 - rint(x1)), &sn, &cn);
-      cs[lane + 32] = make_float2(cn, sn);
+      // |remainder| <= pi: the fast sine and cosine are off by at most 2^-21 there, far below a half
+      // step of the 16-bit results
+      const float kTwoPi = 6.28318530717958648f, r0 = kTwoPi * (float)(x0 - rint(x0)), r1 = kTwoPi * (float)(x1 - rint(x1));
+      cs[lane] = make_float2(__cosf(r0), __sinf(r0));
+      cs[lane + 32] = make_float2(__cosf(r1), __sinf(r1));
     }
     int64_t at = -1;  // byte offset of the token's cell in the pool
     if (slot >= a.n_slots) {
@@ -387,8 +395,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) qk_rope_append_kernel(cons
         }
       }
     };
-    // rows from .. to - 1 of the unit, two at a time, row r to dst + r * pitch
-    auto turn = [&](int from, int to, bool norm, char* dst, int64_t pitch) {
+    // rows from .. to - 1 of the unit, two at a time, row r to dst(r)
+    auto turn = [&](int from, int to, bool norm, auto&& dst) {
       const unsigned char* in = ring + st * unit_bytes + c * 16;
       const int swap = (c < 8 ? 8 : -8) * 16;
 #pragma unroll 4
@@ -400,33 +408,38 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 2) qk_rope_append_kernel(cons
         const float2 p[4] = {unpack2<T>(pw.x), unpack2<T>(pw.y), unpack2<T>(pw.z), unpack2<T>(pw.w)};
         float inv = 1.f;
         if (GAINS && norm) {
-          float2 s2 = make_float2(0.f, 0.f);
+          float ss = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(x[j], x[j], s2);
-          float ss = s2.x + s2.y;
+          for (int j = 0; j < 4; ++j) ss = fmaf(x[j].x, x[j].x, fmaf(x[j].y, x[j].y, ss));
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           inv = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
         }
-        const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x[j] = __ffma2_rn(x[j], own[j], __fmul2_rn(p[j], other[j]));
-          if (GAINS) x[j] = __fmul2_rn(x[j], inv2);
+          x[j].x = fmaf(x[j].x, own[j].x, p[j].x * other[j].x) * inv;
+          x[j].y = fmaf(x[j].y, own[j].y, p[j].y * other[j].y) * inv;
         }
-        *reinterpret_cast<uint4*>(dst + r * pitch) = make_uint4(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y),
+        *reinterpret_cast<uint4*>(dst(r)) = make_uint4(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y),
                                                                 pack2<T>(x[2].x, x[2].y), pack2<T>(x[3].x, x[3].y));
       }
     };
     const int q_end = min(max(a.Hq - h0, 0), nh), k_end = min(max(a.Hq + a.Hkv - h0, 0), nh);
     if (q_end > 0 || (k_end > 0 && at >= 0)) factors(q_end > 0 ? a.q_gain : a.k_gain);
     wait_phase(&full[st], round & 1);
-    if (q_end > 0) turn(0, q_end, a.q_gain != nullptr, a.q_out + t * a.qo_stride + h0 * kRow + c * 16, kRow);
-    if (at >= 0) {
-      if (k_end > q_end) {
-        if (GAINS && q_end > 0) factors(a.k_gain);
-        turn(q_end, k_end, a.k_gain != nullptr, a.kp + at + (h0 - a.Hq) * a.head_stride + c * 16, a.head_stride);
+    char* q_out = a.q_out + t * a.qo_stride + h0 * kRow + c * 16;
+    char* k_out = a.kp + at + (h0 - a.Hq) * a.head_stride + c * 16;
+    if (!GAINS && at >= 0) {
+      // the same factors for queries and keys: one loop
+      turn(0, k_end, false, [&](int r) { return r < q_end ? q_out + r * kRow : k_out + r * a.head_stride; });
+    } else {
+      if (q_end > 0) turn(0, q_end, a.q_gain != nullptr, [&](int r) { return q_out + r * kRow; });
+      if (at >= 0 && k_end > q_end) {
+        if (q_end > 0) factors(a.k_gain);
+        turn(q_end, k_end, a.k_gain != nullptr, [&](int r) { return k_out + r * a.head_stride; });
       }
+    }
+    if (at >= 0) {
 #pragma unroll 2
       for (int r = k_end + (lane >> 4); r < nh; r += 2)
         *reinterpret_cast<uint4*>(a.vp + at + (h0 + r - a.Hq - a.Hkv) * a.head_stride + c * 16) =
@@ -555,22 +568,24 @@ extern "C" vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const vo
   // a token in as few units of at most 18 heads as there are warps for, in smaller ones (an even
   // number of heads, two rows at a time) when tokens are few
   const int heads = Hq + 2 * Hkv;
-  const int64_t warps = 2 * vv::sm_count() * vv::kRopeWarps;
+  const bool gains = q_gain || k_gain;
+  const int cta_warps = gains ? vv::RopeShape<true>::kWarps : vv::RopeShape<false>::kWarps;
+  const int stages = gains ? vv::RopeShape<true>::kStages : vv::RopeShape<false>::kStages;
+  const int64_t warps = 2 * vv::sm_count() * cta_warps;
   int64_t parts = (heads + vv::kRopeHeads - 1) / vv::kRopeHeads;
   parts = std::max(parts, std::min<int64_t>((heads + 1) / 2, warps / T));
   a.heads = (int)((heads + parts - 1) / parts + 1) / 2 * 2;
   a.parts = (heads + a.heads - 1) / a.heads;
   const int64_t units = T * a.parts;
-  const int grid = (int)std::min<int64_t>((units + vv::kRopeWarps - 1) / vv::kRopeWarps, 2 * vv::sm_count());
-  const size_t smem = (size_t)vv::kRopeWarps * vv::kRopeStages * a.heads * D * 2;
+  const int grid = (int)std::min<int64_t>((units + cta_warps - 1) / cta_warps, 2 * vv::sm_count());
+  const size_t smem = (size_t)cta_warps * stages * a.heads * D * 2;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool gains = q_gain || k_gain;
   auto kernel = kv->dtype == VV_F16
                     ? (gains ? vv::qk_rope_append_kernel<__half, true> : vv::qk_rope_append_kernel<__half, false>)
                     : (gains ? vv::qk_rope_append_kernel<__nv_bfloat16, true>
                              : vv::qk_rope_append_kernel<__nv_bfloat16, false>);
   if (smem > (40u << 10))
     VV_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  kernel<<<grid, vv::kRopeWarps * 32, smem, s>>>(a);
+  kernel<<<grid, cta_warps * 32, smem, s>>>(a);
   return vv::cuda_check(cudaGetLastError(), "vv_qk_rope_append launch");
 }
