@@ -5,9 +5,13 @@
 //
 //   out[b, h] = sum_t p_t V_t / sum_t p_t,  p_t = exp(scale q . K_t),  t over prompt ++ own pages
 //
-// Softmax over the union of two key sets splits exactly: with (m, l, o) the maximum, the sum of
+// Softmax over the union of key sets splits exactly: with (m, l, o) the maximum, the sum of
 // exp(s - m) and the weighted sum of values of each part, the union's are M = max(m_i),
-// L = sum l_i e^(m_i - M), O = sum o_i e^(m_i - M).
+// L = sum l_i e^(m_i - M), O = sum o_i e^(m_i - M).  So three kernels, each launched while the one
+// before it still runs (programmatic launch): the shared prompt for all sequences together
+// (attn_shared_tc.cu, nothing to do with the second until the join), the sequences' own pages, and
+// the join of all parts, a warp per output row.  Joining inside the second kernel took longer: a
+// few CTAs hold several heads, and a head's parts are a dozen dependent reads.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,9 +37,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // All keys of all sequences and key-value heads form one list of 16-key chunks, ordered by
 // sequence, head and position; the CTAs (one per SM) take equal runs of it, found from the lengths
 // on the device, so ragged batches load every SM alike (each head counts kEnd chunks more, what it
-// costs to finish one).  A head that lies in one run is finished by its CTA; one that crosses runs
-// leaves partial rows (at most two sets per CTA) and the last of its CTAs to arrive joins them in
-// run order: the result does not depend on who that is.
+// costs to begin and end one).  A head, or the part of it that lies in a run, ends as partial rows
+// (o, m, l) in the workspace; the join kernel puts them together.
 //
 // One warp walks the run ahead of the others: eight lanes look up eight chunks' pages at a time
 // and copy their rows (TMA, 128-byte swizzle) into a ring of 21 chunks, 168 KB on their way per
@@ -73,13 +76,11 @@ struct SharedAttnArgs {
   const void* vp;
   const int32_t* table;
   const int32_t* lens;
-  void* out;
-  float* lse;
-  float* part;       // [CTAs][2][G][kPartRow]: a run's first head (begun in an earlier run), its last
-  unsigned* arrived; // [CTAs]: arrivals for the head that begins in this run and goes on
-  const float* pre_part;  // [Hkv][pre_splits][B * G][kPartRow]: the shared prompt's
-  int pre_splits;    // 0: the prompt's keys, if any, are read here (kpre, vpre, P)
-  int64_t q_stride, out_stride, pre_head, pre_token, page_stride, head_stride, token_stride;
+  float* part;       // [B][Hkv][G][kPartRow]: heads that lie in one run
+  float* run_part;   // [CTAs][2][G][kPartRow]: a run's first head (begun in an earlier run), its last
+  int2* where;       // [B][Hkv]: the run that the head begins in, runs that share it
+  bool shared;       // the prompt has a kernel of its own; else its keys, if any, are read here
+  int64_t q_stride, pre_head, pre_token, page_stride, head_stride, token_stride;
   int B, Hkv, G, P, ps, pages, max_blocks;
   float c;  // scale * log2(e)
 };
@@ -139,13 +140,25 @@ struct OwnMaps {
   CUtensorMap kpre, vpre;  // prompt: dims {64, P, 2, Hkv, 1}, the same box; rows past P read as zeros
 };
 
-// The CTA of n whose run of a list of `total` places holds place x (run c: [total c / n, total (c + 1) / n)).
-__device__ __forceinline__ int run_of(int64_t x, int64_t total, int n) {
-  int c = (int)(x * n / total);
-  while (total * (c + 1) / n <= x) ++c;
-  while (total * c / n > x) --c;
-  return c;
-}
+// `total` places in n runs, the first `more` of them a place longer.
+struct Runs {
+  int64_t len;
+  int more;
+  __device__ Runs(int64_t total, int n) {
+    if (total <= 0x7fffffff) {  // 32-bit division is much shorter
+      len = (unsigned)total / (unsigned)n;
+      more = (int)((unsigned)total % (unsigned)n);
+    } else {
+      len = total / n;
+      more = (int)(total % n);
+    }
+  }
+  __device__ int64_t begin(int c) const { return c * len + min(c, more); }
+  __device__ int of(int64_t x) const {  // the run that holds place x
+    const int64_t longer = more * (len + 1);
+    return x < longer ? (int)(x / (len + 1)) : more + (int)((x - longer) / len);
+  }
+};
 
 // Where a warp is in its CTA's run: chunk t of `chunks` of head g of sequence b.
 struct Walker {
@@ -157,18 +170,18 @@ struct Joined {
   float4 o;
 };
 
-// Joins n parts of a row into r; part k lies at base + k * stride: o[128], m, l.  The maxima and sums
-// of up to KB parts are read one a lane and their rows together, one round trip to L2 a batch.
-template <int KB>
-__device__ __forceinline__ void absorb(Joined& r, const float* base, int n, int64_t stride, int lane) {
+// Joins n parts of a row into r; part(k) points to part k: o[128], m, l.  The maxima and sums of KB
+// parts are read one a lane and their rows together, one round trip to memory a batch.
+template <int KB, typename F>
+__device__ __forceinline__ void absorb(Joined& r, int n, int lane, F&& part) {
   for (int k0 = 0; k0 < n; k0 += KB) {
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < KB && k0 + lane < n) ml = *reinterpret_cast<const float2*>(base + (k0 + lane) * stride + D);
+    if (lane < KB && k0 + lane < n) ml = *reinterpret_cast<const float2*>(part(k0 + lane) + D);
     float4 v[KB];
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k0 + k < n) v[k] = *reinterpret_cast<const float4*>(base + (k0 + k) * stride + lane * 4);
+      if (k0 + k < n) v[k] = *reinterpret_cast<const float4*>(part(k0 + k) + lane * 4);
     }
     const float mn = fmaxf(r.m, warp_max(ml.x)), ref = mn == -INFINITY ? 0.f : mn;
     const float w0 = exp2_fast(r.m - ref), w = exp2_fast(ml.x - ref);
@@ -193,10 +206,10 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
   __shared__ int64_t warp_sum_s[kOwnThreads / 32];
   __shared__ Walker s_first;
   __shared__ int s_bad[kOwnStages];  // the chunk's page does not exist
-  __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.G;
+  pdl_launch_dependents();  // the join kernel waits for this one's end by itself
   const int cap = (int)min((int64_t)a.max_blocks * a.ps, (int64_t)0x7fffffff);
-  const int npre = a.pre_splits ? 0 : (a.P + kChunk - 1) / kChunk;
+  const int npre = a.shared ? 0 : (a.P + kChunk - 1) / kChunk;
   if (tid < kOwnStages) {
     mbar_init(&full[tid], 1);
     mbar_init(&empty[tid], 1);
@@ -233,7 +246,8 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
     pdl_wait();
     return;
   }
-  const int64_t x0 = total * cta / n_run, x1 = total * (cta + 1) / n_run;
+  const Runs runs(total, n_run);
+  const int64_t x0 = runs.begin(cta), x1 = runs.begin(cta + 1);
   if (before <= x0 && x0 < before + mine * a.Hkv) {
     int64_t at = before;
     for (int b = b_lo;; ++b) {
@@ -317,7 +331,6 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
   }
 
   auto consumers_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kOwnWarps * 32) : "memory"); };
-  bool waited = false;  // for the prompt's kernel
   for_each_head([&](const Walker& w, int64_t x, int n, int c) {
     // the group's queries as A fragments, 8 steps of 16 dimensions; rows past G are zero
     uint32_t qf[8][4];
@@ -421,32 +434,14 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     }
 
-    // ---- the head ends here, or goes on in the next run: which runs share it
-    int c0 = cta, parts = 1;
-    const int64_t h0 = x - w.t, h1 = h0 + w.chunks;
-    if (h0 < x0) c0 = run_of(h0, total, n_run);
-    if (h0 < x0 || h1 > x1) parts = (h1 > x1 ? run_of(h1 - 1, total, n_run) : cta) - c0 + 1;
-    float* part = a.part + ((int64_t)cta * 2 + (c0 == cta ? 1 : 0)) * G * kPartRow;
-    const int64_t all = (int64_t)a.B * G;
-    const float* pre = a.pre_part + ((int64_t)w.g * a.pre_splits * all + (int64_t)w.b * G) * kPartRow;
-    auto finish = [&](Joined& r, int row) {
-      if (!waited) {
-        pdl_wait();  // the prompt's parts are complete
-        waited = true;
-      }
-      absorb<16>(r, pre + row * kPartRow, a.pre_splits, all * kPartRow, lane);
-      const int h = w.g * G + row;
-      // l is 0 where no key has a weight; a NaN score makes l NaN and goes on to the result
-      const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
-      T* dst = static_cast<T*>(a.out) + (int64_t)w.b * a.out_stride + h * D + lane * 4;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_pair<T>(r.o.x * inv, r.o.y * inv), pack_pair<T>(r.o.z * inv, r.o.w * inv));
-      if (a.lse && lane == 0)
-        a.lse[(int64_t)w.b * a.Hkv * G + h] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
-    };
-    // join the warps' rows through shared memory, eight rows at a time, a row per warp
+    // ---- the head ends here, or goes on in the next run: its rows, joined over the warps through
+    // shared memory (eight at a time, a row per warp), to where the join kernel looks for them
+    const int64_t h0 = x - w.t, h1 = h0 + w.chunks, head = (int64_t)w.b * a.Hkv + w.g;
+    const bool begun = h0 >= x0, whole = begun && h1 <= x1;
+    if (begun && tid == 0) a.where[head] = make_int2(cta, whole ? 1 : runs.of(h1 - 1) - cta + 1);
+    float* to = (whole ? a.part + head * G * kPartRow : a.run_part + ((int64_t)cta * 2 + (begun ? 1 : 0)) * G * kPartRow);
 #pragma unroll
     for (int h = 0; h < (WIDE ? 2 : 1); ++h) {
-      if (h == 1) consumers_sync();  // the first eight have been read
       float* d = sp + (warp * 8 + (lane >> 2)) * kPartRow;
 #pragma unroll
       for (int k = 0; k < 16; ++k)
@@ -455,55 +450,76 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
       consumers_sync();
       for (int row = warp; row < min(G - 8 * h, 8); row += kOwnWarps) {
         Joined r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-        absorb<kOwnWarps>(r, sp + row * kPartRow, kOwnWarps, 8 * kPartRow, lane);
-        if (parts == 1) {
-          finish(r, 8 * h + row);
-        } else {
-          float* to = part + (8 * h + row) * kPartRow;
-          *reinterpret_cast<float4*>(to + lane * 4) = r.o;
-          if (lane == 0) *reinterpret_cast<float2*>(to + D) = make_float2(r.m, r.l);
-        }
+        absorb<kOwnWarps>(r, kOwnWarps, lane, [&](int k) { return sp + (k * 8 + row) * kPartRow; });
+        float* at = to + (8 * h + row) * kPartRow;
+        *reinterpret_cast<float4*>(at + lane * 4) = r.o;
+        if (lane == 0) *reinterpret_cast<float2*>(at + D) = make_float2(r.m, r.l);
       }
+      consumers_sync();  // the join buffer is free again
     }
-    if (parts > 1) {
-      __threadfence();
-      consumers_sync();
-      if (tid == 0) s_last = atomicAdd(&a.arrived[c0], 1u) == (unsigned)(parts - 1);
-      consumers_sync();
-      if (s_last) {
-        __threadfence();
-        if (tid == 0) a.arrived[c0] = 0;
-        for (int row = warp; row < G; row += kOwnWarps) {
-          Joined r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-          // the set that c0 began last, then the first sets of the CTAs after it
-          const float* p0 = a.part + ((int64_t)c0 * 2 * G + row) * kPartRow;
-          absorb<1>(r, p0 + G * kPartRow, 1, 0, lane);
-          absorb<16>(r, p0 + 2 * G * kPartRow, parts - 1, 2 * (int64_t)G * kPartRow, lane);
-          finish(r, row);
-        }
-      }
-    }
-    consumers_sync();  // the join buffer is free again
   });
-  if (!waited) pdl_wait();
+  pdl_wait();  // the join reads the prompt's parts: it may only start after both kernels
+}
+
+// --------------------------------------------------------------------------------------- join
+//
+// A warp per output row: where its own parts lie, then all parts (own and the prompt's) together,
+// four dimensions a lane; two dependent reads of memory, whatever the number of parts up to 16.
+struct JoinArgs {
+  const float* part;
+  const float* run_part;
+  const int2* where;
+  const float* pre_part;  // [Hkv][pre_splits][B * G][kPartRow]
+  const int32_t* lens;
+  void* out;
+  float* lse;
+  int64_t out_stride;
+  int B, Hkv, G, pre_splits;
+};
+constexpr int kJoinWarps = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ JoinArgs a) {
+  const int lane = threadIdx.x & 31, Hq = a.Hkv * a.G;
+  const int64_t row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int b = (int)(row / Hq), h = (int)(row - (int64_t)b * Hq), g = h / a.G, i = h - g * a.G;
+  const bool live = row < (int64_t)a.B * Hq && a.lens[min(b, a.B - 1)] >= 0;  // not a padding row
+  pdl_wait();
+  if (!live) return;
+  const int64_t head = (int64_t)b * a.Hkv + g, all = (int64_t)a.B * a.G;
+  const int2 at = a.where[head];
+  const float* pre = a.pre_part + ((int64_t)g * a.pre_splits * all + (int64_t)b * a.G + i) * kPartRow;
+  Joined r = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  absorb<16>(r, at.y + a.pre_splits, lane, [&](int k) {
+    if (k >= at.y) return pre + (k - at.y) * all * kPartRow;
+    if (at.y == 1) return a.part + (head * a.G + i) * kPartRow;
+    // the set that the first run ended with, then the sets that the runs after it began with
+    return a.run_part + ((2 * (int64_t)(at.x + k) + (k == 0)) * a.G + i) * kPartRow;
+  });
+  // l is 0 where no key has a weight; a NaN score makes l NaN and goes on to the result
+  const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+  T* dst = static_cast<T*>(a.out) + (int64_t)b * a.out_stride + h * D + lane * 4;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_pair<T>(r.o.x * inv, r.o.y * inv), pack_pair<T>(r.o.z * inv, r.o.w * inv));
+  if (a.lse && lane == 0) a.lse[(int64_t)b * Hq + h] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
 }
 
 struct Plan {
   int ctas, pre_splits, pre_per;
-  size_t part, pre_part, total;  // byte offsets in the workspace; the arrival counters come first
+  size_t run_part, part, pre_part, total;  // byte offsets in the workspace; `where` comes first
 };
 Plan plan_of(int B, int Hkv, int G, int P, int64_t max_own) {
   Plan p = {};
   // One sequence shares nothing, and a prompt of a few chunks costs less to read again than a
-  // second kernel: there the prompt's keys are the first tiles of every sequence.
+  // second kernel: there the prompt's keys are the first chunks of every sequence.
   const bool shared = B > 1 && P >= kMinShared;
   if (shared) prefix_tc_split(B * G, Hkv, P, &p.pre_splits, &p.pre_per);
   const int64_t chunks = (max_own + kChunk - 1) / kChunk + (shared ? 0 : (P + kChunk - 1) / kChunk);
   p.ctas = (int)std::min<int64_t>(sm_count(), std::max<int64_t>(chunks, 1) * B * Hkv);
-  const size_t row = kPartRow * sizeof(float);
-  p.part = ((size_t)p.ctas * 4 + 255) / 256 * 256;
-  p.pre_part = p.part + (size_t)p.ctas * 2 * G * row;
-  p.total = p.pre_part + (size_t)p.pre_splits * B * Hkv * G * row;
+  const size_t set = (size_t)G * kPartRow * sizeof(float), heads = (size_t)B * Hkv;
+  p.run_part = (heads * sizeof(int2) + 255) / 256 * 256;
+  p.part = p.run_part + p.ctas * 2 * set;
+  p.pre_part = p.part + heads * set;
+  p.total = p.pre_part + p.pre_splits * heads * set;
   return p;
 }
 
@@ -527,10 +543,14 @@ bool page_map(CUtensorMap* tm, const void* base, int dtype, int64_t tokens, int6
 }
 
 template <typename T, bool WIDE>
-cudaError_t launch_own(const OwnMaps& mp, const SharedAttnArgs& a, int ctas, cudaStream_t s) {
+cudaError_t launch_own(const OwnMaps& mp, const SharedAttnArgs& a, const JoinArgs& j, int ctas, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(own_attn_kernel<T, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem);
   if (e != cudaSuccess) return e;
-  return launch(own_attn_kernel<T, WIDE>, dim3(ctas), dim3(kOwnThreads), kOwnSmem, s, a.pre_splits > 0, mp, a);
+  e = launch(own_attn_kernel<T, WIDE>, dim3(ctas), dim3(kOwnThreads), kOwnSmem, s, a.shared, mp, a);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)j.B * j.Hkv * j.G;
+  return launch(join_kernel<T>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, s,
+                true, j);
 }
 
 bool sizes_ok(int B, int Hq, int Hkv, int D_, int P) {
@@ -593,14 +613,13 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
   a.vp = kv->v;
   a.table = block_tables;
   a.lens = own_lens;
-  a.out = out;
-  a.lse = lse;
-  a.arrived = static_cast<unsigned*>(ws);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
-  a.pre_part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.pre_part);
-  a.pre_splits = p.pre_splits;
+  char* base = static_cast<char*>(ws);
+  a.where = reinterpret_cast<int2*>(base);
+  a.run_part = reinterpret_cast<float*>(base + p.run_part);
+  a.part = reinterpret_cast<float*>(base + p.part);
+  a.shared = p.pre_splits > 0;
+  float* pre_part = reinterpret_cast<float*>(base + p.pre_part);
   a.q_stride = q_stride;
-  a.out_stride = out_stride;
   a.pre_head = prefix_head_stride;
   a.pre_token = prefix_token_stride;
   a.page_stride = kv->page_stride;
@@ -620,7 +639,7 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
     t.q = q;
     t.k = k_prefix;
     t.v = v_prefix;
-    t.part = const_cast<float*>(a.pre_part);
+    t.part = pre_part;
     t.q_stride = q_stride;
     t.head = prefix_head_stride;
     t.token = prefix_token_stride;
@@ -641,9 +660,10 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
     ok = vv::page_map(&mp.kpre, k_prefix, kv->dtype, prefix_len, Hkv, 1, prefix_token_stride, prefix_head_stride, 0) &&
          vv::page_map(&mp.vpre, v_prefix, kv->dtype, prefix_len, Hkv, 1, prefix_token_stride, prefix_head_stride, 0);
   if (!ok) return vv::set_error(VV_ERR_CUDA, "vv_gqa_prefix_attn: tensor map encoding failed");
+  const vv::JoinArgs j = {a.part, a.run_part, a.where, pre_part, own_lens, out, lse, out_stride, B, Hkv, G, p.pre_splits};
   const bool f16 = kv->dtype == VV_F16, wide = G > 8;
-  const cudaError_t e = f16 ? (wide ? vv::launch_own<__half, true>(mp, a, p.ctas, s) : vv::launch_own<__half, false>(mp, a, p.ctas, s))
-                            : (wide ? vv::launch_own<__nv_bfloat16, true>(mp, a, p.ctas, s)
-                                    : vv::launch_own<__nv_bfloat16, false>(mp, a, p.ctas, s));
+  const cudaError_t e = f16 ? (wide ? vv::launch_own<__half, true>(mp, a, j, p.ctas, s) : vv::launch_own<__half, false>(mp, a, j, p.ctas, s))
+                            : (wide ? vv::launch_own<__nv_bfloat16, true>(mp, a, j, p.ctas, s)
+                                    : vv::launch_own<__nv_bfloat16, false>(mp, a, j, p.ctas, s));
   return vv::cuda_check(e, "vv_gqa_prefix_attn launch");
 }
