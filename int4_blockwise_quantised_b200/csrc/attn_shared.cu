@@ -8,10 +8,10 @@
 // Softmax over the union of key sets splits exactly: with (m, l, o) the maximum, the sum of
 // exp(s - m) and the weighted sum of values of each part, the union's are M = max(m_i),
 // L = sum l_i e^(m_i - M), O = sum o_i e^(m_i - M).  So three kernels, each launched while the one
-// before it still runs (programmatic launch): the shared prompt for all sequences together
-// (attn_shared_tc.cu, nothing to do with the second until the join), the sequences' own pages, and
-// the join of all parts, a warp per output row.  Joining inside the second kernel took longer: a
-// few CTAs hold several heads, and a head's parts are a dozen dependent reads.
+// before it still runs (programmatic launch): the sequences' own pages, the shared prompt for all
+// sequences together (attn_shared_tc.cu, nothing to do with the first; it ends after it), and the
+// join of all parts, a warp per output row.  Joining at the end of the first two took longer: a few
+// CTAs hold several heads, and a head's parts are a dozen dependent reads.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -63,8 +63,8 @@ constexpr int kOwnStages = 3 * kOwnWarps;              // a multiple: a stage ha
 static_assert(kOwnStages % kOwnWarps == 0, "a stage belongs to one consumer warp");
 constexpr int kBatch = 8;                             // chunks copied at a time
 static_assert(kBatch <= kOwnStages, "a batch never waits for itself");
-constexpr int kEnd = 40;                              // a head's end, in chunks
-constexpr int kMinRun = 2 * kOwnWarps;                // least chunks of a run
+constexpr int kEnd = 10;                              // a head's beginning and end, in chunks
+constexpr int kMinRun = 4 + kEnd;                     // least places of a run: a short head alone
 constexpr int kMinShared = 128;                       // least prompt with a kernel of its own
 constexpr int kOwnSmem = kOwnStages * kStageBytes + kOwnWarps * 8 * kPartRow * 4 + 1024;
 
@@ -207,9 +207,13 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
   __shared__ Walker s_first;
   __shared__ int s_bad[kOwnStages];  // the chunk's page does not exist
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = a.G;
-  pdl_launch_dependents();  // the join kernel waits for this one's end by itself
+  pdl_launch_dependents();  // the next kernels need nothing of this one until their end
   const int cap = (int)min((int64_t)a.max_blocks * a.ps, (int64_t)0x7fffffff);
   const int npre = a.shared ? 0 : (a.P + kChunk - 1) / kChunk;
+  if (tid == kOwnWarps * 32) {
+    tc::prefetch_map(&mp.k);
+    tc::prefetch_map(&mp.v);
+  }
   if (tid < kOwnStages) {
     mbar_init(&full[tid], 1);
     mbar_init(&empty[tid], 1);
@@ -240,12 +244,9 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
   before = (before + scan - mine) * a.Hkv;  // places before this thread's sequences
   total *= a.Hkv;
   // runs: all CTAs, or fewer when the list is short
-  const int n_run = (int)min((int64_t)gridDim.x, max(total / (kMinRun + kEnd), (int64_t)1));
+  const int n_run = (int)min((int64_t)gridDim.x, max(total / kMinRun, (int64_t)1));
   const int cta = blockIdx.x;
-  if (total == 0 || cta >= n_run) {
-    pdl_wait();
-    return;
-  }
+  if (total == 0 || cta >= n_run) return;
   const Runs runs(total, n_run);
   const int64_t x0 = runs.begin(cta), x1 = runs.begin(cta + 1);
   if (before <= x0 && x0 < before + mine * a.Hkv) {
@@ -326,7 +327,6 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         page = next;
       }
     });
-    pdl_wait();
     return;
   }
 
@@ -458,7 +458,6 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
       consumers_sync();  // the join buffer is free again
     }
   });
-  pdl_wait();  // the join reads the prompt's parts: it may only start after both kernels
 }
 
 // --------------------------------------------------------------------------------------- join
@@ -543,11 +542,16 @@ bool page_map(CUtensorMap* tm, const void* base, int dtype, int64_t tokens, int6
 }
 
 template <typename T, bool WIDE>
-cudaError_t launch_own(const OwnMaps& mp, const SharedAttnArgs& a, const JoinArgs& j, int ctas, cudaStream_t s) {
+cudaError_t launch_all(const OwnMaps& mp, const SharedAttnArgs& a, const PrefixTcArgs* t, const JoinArgs& j, int ctas,
+                       cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(own_attn_kernel<T, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem);
   if (e != cudaSuccess) return e;
-  e = launch(own_attn_kernel<T, WIDE>, dim3(ctas), dim3(kOwnThreads), kOwnSmem, s, a.shared, mp, a);
+  e = launch(own_attn_kernel<T, WIDE>, dim3(ctas), dim3(kOwnThreads), kOwnSmem, s, false, mp, a);
   if (e != cudaSuccess) return e;
+  if (t) {
+    e = launch_prefix_tc(*t, s);
+    if (e != cudaSuccess) return e;
+  }
   const int64_t rows = (int64_t)j.B * j.Hkv * j.G;
   return launch(join_kernel<T>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, s,
                 true, j);
@@ -634,8 +638,9 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
   a.max_blocks = max_blocks;
   a.c = scale * vv::kLog2e;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.pre_splits) {
-    vv::PrefixTcArgs t = {};
+  vv::PrefixTcArgs t = {};
+  const vv::PrefixTcArgs* pre = p.pre_splits ? &t : nullptr;
+  if (pre) {
     t.q = q;
     t.k = k_prefix;
     t.v = v_prefix;
@@ -651,7 +656,6 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
     t.per = p.pre_per;
     t.c = a.c;
     t.dtype = kv->dtype;
-    VV_CUDA(vv::launch_prefix_tc(t, s));
   }
   vv::OwnMaps mp = {};
   bool ok = vv::page_map(&mp.k, kv->k, kv->dtype, kv->page_size, Hkv, kv->pages, kv->token_stride, kv->head_stride, kv->page_stride) &&
@@ -662,8 +666,8 @@ extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t
   if (!ok) return vv::set_error(VV_ERR_CUDA, "vv_gqa_prefix_attn: tensor map encoding failed");
   const vv::JoinArgs j = {a.part, a.run_part, a.where, pre_part, own_lens, out, lse, out_stride, B, Hkv, G, p.pre_splits};
   const bool f16 = kv->dtype == VV_F16, wide = G > 8;
-  const cudaError_t e = f16 ? (wide ? vv::launch_own<__half, true>(mp, a, j, p.ctas, s) : vv::launch_own<__half, false>(mp, a, j, p.ctas, s))
-                            : (wide ? vv::launch_own<__nv_bfloat16, true>(mp, a, j, p.ctas, s)
-                                    : vv::launch_own<__nv_bfloat16, false>(mp, a, j, p.ctas, s));
+  const cudaError_t e = f16 ? (wide ? vv::launch_all<__half, true>(mp, a, pre, j, p.ctas, s) : vv::launch_all<__half, false>(mp, a, pre, j, p.ctas, s))
+                            : (wide ? vv::launch_all<__nv_bfloat16, true>(mp, a, pre, j, p.ctas, s)
+                                    : vv::launch_all<__nv_bfloat16, false>(mp, a, pre, j, p.ctas, s));
   return vv::cuda_check(e, "vv_gqa_prefix_attn launch");
 }

@@ -26,7 +26,7 @@
 // them out.
 // The weights are rounded to the element type because the tensor cores multiply 16-bit operands;
 // their sum l is taken before that rounding.  The tile's partial rows (o, m, l) go to the workspace
-// in fp32; the caller's second kernel joins the parts.
+// in fp32; the join kernel puts the parts together.
 // Every mbarrier wait is bounded; tensor memory is released before the CTA exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_free + 2;            // [2]
   uint64_t* pv_done = p_full + 2;           // [2] also frees the V stage
   uint64_t* o_done = pv_done + 2;           // all products: one phase, waited for by both groups
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 1);
+  uint64_t* v_go = o_done + 1;              // the first K tile is here: one phase
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_go + 1);
   float(*m_row)[BM] = reinterpret_cast<float(*)[BM]>(smem + kTiles * kTile + kBarBytes);  // [2][BM]
   float2(*ml)[BM] = reinterpret_cast<float2(*)[BM]>(smem + kTiles * kTile + kBarBytes + 2 * BM * 4);
 
@@ -110,8 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int blocks = (a.P + BN - 1) / BN;
   const int j0 = split * a.per, n = min(a.per, blocks - j0);  // n >= 1 by the launch's grid
 
-  // the second kernel's own work (the sequences' pages) needs nothing of this one
-  pdl_launch_dependents();
+  pdl_launch_dependents();  // the join waits for this kernel's end by itself
   auto load_k = [&](int j) {
     const int st = j % kKStages;
     unsigned char* kt = sK + st * kTile;
@@ -139,10 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(o_done, 1);
+    mbar_init(v_go, 1);
     fence_mbar_init();
-    // the rings' first fill is on its way before the rest of the CTA is ready
-    for (int j = 0; j < min(n, kKStages); ++j) load_k(j);
-    for (int j = 0; j < min(n, kVStages); ++j) load_v(j);
+    load_k(0);  // on its way before the rest of the CTA is ready
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -180,16 +179,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      for (int j = kKStages; j < n; ++j) {
-        wait_phase(&k_empty[j % kKStages], (j / kKStages - 1) & 1);
+      // all CTAs begin at once: the others' first tiles come before this one's second
+      auto first_tile = [&] {
+        wait_phase(&k_full[0], 0);
+        mbar_arrive(v_go);
+      };
+      for (int j = 1; j < n; ++j) {
+        if (j >= kKStages) wait_phase(&k_empty[j % kKStages], (j / kKStages - 1) & 1);
+        if (j == 2) first_tile();
         load_k(j);
       }
+      if (n <= 2) first_tile();
     }
     __syncwarp();
   } else if (warp == 2) {
     if (lane == 0) {
-      for (int j = kVStages; j < n; ++j) {
-        wait_phase(&pv_done[j & 1], ((j >> 1) - 1) & 1);
+      wait_phase(v_go, 0);
+      for (int j = 0; j < n; ++j) {
+        if (j >= kVStages) wait_phase(&pv_done[j & 1], ((j >> 1) - 1) & 1);
         load_v(j);
       }
     }
@@ -348,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_before();
   __syncthreads();
+  pdl_wait();  // the join reads the own pages' parts too: it may only start after both kernels
   if (warp == 1) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -360,22 +368,21 @@ cudaError_t launch_t(const KvMaps& mp, const PrefixTcArgs& a, cudaStream_t s) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.B * a.G + BM - 1) / BM, a.splits, a.Hkv);
-  prefix_tc_kernel<T><<<grid, kThreads, kSmem, s>>>(mp, a);
-  return cudaGetLastError();
+  return launch(prefix_tc_kernel<T>, grid, dim3(kThreads), kSmem, s, true, mp, a);
 }
 
 }  // namespace
 
 void prefix_tc_split(int rows, int Hkv, int P, int* splits, int* per) {
-  // Cost in blocks of 128 keys (about 0.85 us each): waves x (a part's blocks + 4 for its start and
-  // end), and 1/16 for each part that the second kernel has to join.
+  // Cost in blocks of 128 keys (about 0.8 us each): waves x (a part's blocks + 4 for its start and
+  // end), and one for each further 16 parts that the join has to read.
   const int64_t tiles = (int64_t)((rows + BM - 1) / BM) * Hkv, sms = sm_count();
   const int blocks = (P + BN - 1) / BN;
   int64_t best = INT64_MAX;
   const int most = (int)std::min<int64_t>(blocks, std::max<int64_t>(8, sms / tiles));
   for (int s = 1; s <= most; ++s) {
     const int p = (blocks + s - 1) / s, used = (blocks + p - 1) / p;
-    const int64_t cost = (tiles * used + sms - 1) / sms * (p + 4) * 16 + used;
+    const int64_t cost = (tiles * used + sms - 1) / sms * (p + 4) + used / 16;
     if (cost < best) {
       best = cost;
       *splits = used;
