@@ -364,8 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <typename T>
 cudaError_t launch_t(const KvMaps& mp, const PrefixTcArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  cudaError_t e = allow_smem<prefix_tc_kernel<T>>(kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.B * a.G + BM - 1) / BM, a.splits, a.Hkv);
   return launch(prefix_tc_kernel<T>, grid, dim3(kThreads), kSmem, s, true, mp, a);
@@ -375,14 +374,14 @@ cudaError_t launch_t(const KvMaps& mp, const PrefixTcArgs& a, cudaStream_t s) {
 
 void prefix_tc_split(int rows, int Hkv, int P, int* splits, int* per) {
   // Cost in blocks of 128 keys (about 0.8 us each): waves x (a part's blocks + 4 for its start and
-  // end), and one for each further 16 parts that the join has to read.
+  // end), and one for each further 32 parts that the join has to read.
   const int64_t tiles = (int64_t)((rows + BM - 1) / BM) * Hkv, sms = sm_count();
   const int blocks = (P + BN - 1) / BN;
   int64_t best = INT64_MAX;
   const int most = (int)std::min<int64_t>(blocks, std::max<int64_t>(8, sms / tiles));
   for (int s = 1; s <= most; ++s) {
     const int p = (blocks + s - 1) / s, used = (blocks + p - 1) / p;
-    const int64_t cost = (tiles * used + sms - 1) / sms * (p + 4) + used / 16;
+    const int64_t cost = (tiles * used + sms - 1) / sms * (p + 4) + used / 32;
     if (cost < best) {
       best = cost;
       *splits = used;

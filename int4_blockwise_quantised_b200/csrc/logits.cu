@@ -327,8 +327,7 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
 template <typename T>
 cudaError_t launch_logits(const LogitsArgs& a, int B, cudaStream_t s) {
   const size_t smem = (a.r.tokens ? kSlice * 4 : 0) + (a.r.bias_ids && !a.packed ? kSlice * 4 : 0);
-  cudaError_t e = cudaFuncSetAttribute(logits_process_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSlice * 8);
+  cudaError_t e = allow_smem<logits_process_kernel<T>>(kSlice * 8);
   if (e != cudaSuccess) return e;
   logits_process_kernel<T><<<dim3((a.V + kSlice - 1) / kSlice, B), kLogitThreads, smem, s>>>(a);
   return cudaGetLastError();

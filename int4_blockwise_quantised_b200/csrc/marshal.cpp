@@ -195,16 +195,34 @@ PyObject* paged_plan(Args& a) {
   const at::Tensor* given[5];
   for (auto& g : given) g = a.tensor_or_none("out");
   if (mt < 1) refuse("%s: max_tokens=%lld", a.who, (long long)mt);
-  at::Tensor made[5];
   const int64_t sizes[5] = {B, B + 1, mt, mt, 1};
   void* out[5];
-  for (int i = 0; i < 5; ++i) {
-    const auto type = i == 2 ? kI64 : kI32;
-    if (!given[i]) {
-      made[i] = p.empty({sizes[i]}, type);
+  at::Tensor made[5];
+  if (!given[0] && !given[1] && !given[2] && !given[3] && !given[4]) {
+    // one allocation, slots first: five took 8.3 us of host time a call
+    int64_t at[5], words = 0;
+    for (int i : {2, 0, 1, 3, 4}) {
+      at[i] = words;
+      words += ((i == 2 ? 2 : 1) * sizes[i] + 3) / 4 * 4;
+    }
+    made[0] = p.empty({words}, kI32);
+    int32_t* base = made[0].data_ptr<int32_t>();
+    for (int i = 4; i >= 0; --i) {
+      const auto type = at::scalarTypeToTypeMeta(i == 2 ? kI64 : kI32);
+      at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(made[0].storage()), made[0].key_set(), type);
+      t.unsafeGetTensorImpl()->set_storage_offset(i == 2 ? at[i] / 2 : at[i]);
+      t.unsafeGetTensorImpl()->set_sizes_contiguous({sizes[i]});
+      out[i] = base + at[i];
+      made[i] = std::move(t);
       given[i] = &made[i];
-      out[i] = made[i].data_ptr();
-    } else {
+    }
+  } else {
+    for (int i = 0; i < 5; ++i) {
+      const auto type = i == 2 ? kI64 : kI32;
+      if (!given[i]) {
+        made[i] = p.empty({sizes[i]}, type);
+        given[i] = &made[i];
+      }
       out[i] = p.dense<void>("out", given[i], type, {sizes[i]});
     }
   }

@@ -454,6 +454,15 @@ __global__ void __launch_bounds__(RopeShape<GAINS>::kWarps * 32, 2)
   }
 }
 
+template <typename T, bool GAINS>
+cudaError_t launch_rope(const RopeArgs& a, int grid, size_t smem, cudaStream_t s) {
+  using Shape = RopeShape<GAINS>;
+  const cudaError_t e = allow_smem<qk_rope_append_kernel<T, GAINS>>(Shape::kWarps * Shape::kStages * kRopeHeads * 256);
+  if (e != cudaSuccess) return e;
+  qk_rope_append_kernel<T, GAINS><<<grid, Shape::kWarps * 32, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 }  // namespace vv
 
@@ -498,9 +507,7 @@ extern "C" vv_status vv_paged_plan(const int32_t* lens, const int32_t* new_lens,
                     offsets, slots, positions, cursor_out, B, prefix_len,
                     page_size, n_free, pages, max_blocks, max_tokens, magic, shift};
   const size_t smem = (size_t)((B + 4) & ~3) * 12;
-  if (smem > (48u << 10))
-    VV_CUDA(cudaFuncSetAttribute(vv::paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem));
+  VV_CUDA(vv::allow_smem<vv::paged_plan_kernel>((vv::kPlanMaxB + 4) * 12));
   // one CTA per 2048 tokens, at most one per SM: each repeats the scan, and three per SM measured
   // 16.4 us where one takes less for 4096 requests with 778k tokens
   const int64_t per = vv::kPlanThreads * 4;
@@ -564,7 +571,11 @@ extern "C" vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const vo
   a.ps = kv->page_size;
   a.eps = eps;
   const double kTwoPi = 6.283185307179586476925286766559;
-  for (int i = 0; i < D / 2; ++i) a.turns[i] = std::pow((double)theta, -2.0 * i / D) / kTwoPi;
+  a.turns[0] = 1.0 / kTwoPi;
+  for (int n = 1; n < D / 2; n *= 2) {  // theta^(-2 i / D) from the powers of i's bits
+    const double f = std::pow((double)theta, -2.0 * n / D);
+    for (int i = 0; i < n; ++i) a.turns[n + i] = a.turns[i] * f;
+  }
   // a token in as few units of at most 18 heads as there are warps for, in smaller ones (an even
   // number of heads, two rows at a time) when tokens are few
   const int heads = Hq + 2 * Hkv;
@@ -580,12 +591,9 @@ extern "C" vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const vo
   const int grid = (int)std::min<int64_t>((units + cta_warps - 1) / cta_warps, 2 * vv::sm_count());
   const size_t smem = (size_t)cta_warps * stages * a.heads * D * 2;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  auto kernel = kv->dtype == VV_F16
-                    ? (gains ? vv::qk_rope_append_kernel<__half, true> : vv::qk_rope_append_kernel<__half, false>)
-                    : (gains ? vv::qk_rope_append_kernel<__nv_bfloat16, true>
-                             : vv::qk_rope_append_kernel<__nv_bfloat16, false>);
-  if (smem > (40u << 10))
-    VV_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  kernel<<<grid, cta_warps * 32, smem, s>>>(a);
-  return vv::cuda_check(cudaGetLastError(), "vv_qk_rope_append launch");
+  const bool f16 = kv->dtype == VV_F16;
+  const cudaError_t e = f16 ? (gains ? vv::launch_rope<__half, true>(a, grid, smem, s) : vv::launch_rope<__half, false>(a, grid, smem, s))
+                            : (gains ? vv::launch_rope<__nv_bfloat16, true>(a, grid, smem, s)
+                                     : vv::launch_rope<__nv_bfloat16, false>(a, grid, smem, s));
+  return vv::cuda_check(e, "vv_qk_rope_append launch");
 }

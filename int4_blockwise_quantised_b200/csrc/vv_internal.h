@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cstdio>
 #include <utility>
 
@@ -58,6 +59,21 @@ inline vv_status check_paged_kv(const vv_paged_kv* kv, int Hkv, int D, const cha
 
 // Number of SMs of the current device (cached per device).
 int sm_count();
+
+// Allows KERNEL `bytes` of dynamic shared memory, once per device: always its most, so that calls of
+// two threads never lower each other's.
+template <auto KERNEL>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Launch with the programmatic-stream-serialization attribute when `pdl` is set.
 template <typename... KArgs, typename... Args>
