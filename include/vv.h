@@ -220,15 +220,16 @@ typedef struct vv_paged_kv {
  *   token j of request b is row offsets[b] + j: slots = table[b, i / page_size] * page_size +
  *   i % page_size and positions = prefix_len + i with i = lens[b] + j;
  *   rows offsets[B] .. max_tokens-1 are padding: slot -1, position 0;
- *   *cursor_out = *cursor + pages taken.
+ *   *cursor_out = *cursor + pages taken;
+ *   lens[b] < 0 with new_lens[b] == 0 is a padding row: nothing is appended, lens_out[b] = lens[b].
  * lens, new_lens device int32 [B]; free_pages device int32 [n_free] (may be NULL when n_free is
  * 0); cursor device int32 [1] or NULL (0); block_tables device int32 [B, max_blocks]; lens_out
  * device int32 [B]; offsets device int32 [B + 1]; slots device int64 [max_tokens]; positions
  * device int32 [max_tokens]; cursor_out device int32 [1].  Pages are numbers in [0, pages).
  * lens_out and cursor_out must not overlap lens, new_lens and cursor.  page_size >= 1 (any),
  * 1 <= B <= 16384.
- * On the device: a negative length, one whose position would pass 2^31 - 1, or a page number
- * outside [0, pages) records VV_ERR_RANGE; more new tokens than max_tokens, more pages than
+ * On the device: any other negative length, one whose position would pass 2^31 - 1, or a page
+ * number outside [0, pages) records VV_ERR_RANGE; more new tokens than max_tokens, more pages than
  * free_pages holds or a table longer than max_blocks records VV_ERR_CAPACITY (vv_sync_status
  * reports either).  Nothing out of bounds is then read or written; tokens without a page get
  * slot -1, table entries without one -1, rows past max_tokens are dropped, and a request with a

@@ -328,6 +328,7 @@ def vv_paged_plan(lens, new_lens, block_tables, free_pages, page_size, pages, ma
 
     lens, new_lens int32 [B]; block_tables int32 [B, max_blocks], updated in place; free_pages
     int32 [n] of page numbers in [0, pages), taken from index *cursor (int32 [1], None: 0) on.
+    lens < 0 with new_lens 0: a padding row, kept as it is.
     Returns PagedPlan(lens int32 [B], offsets int32 [B + 1], slots int64 [max_tokens], positions
     int32 [max_tokens], cursor int32 [1]); `out` may give such a tuple to write into."""
     args = (lens, new_lens, block_tables, free_pages, page_size, pages, max_tokens, prefix_len,

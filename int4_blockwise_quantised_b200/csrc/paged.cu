@@ -96,12 +96,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
     int nt = 0, np = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      fresh[i] = 0;
       if (len[i] < 0 || add[i] < 0 || (int64_t)len[i] + add[i] + a.prefix > 0x7fffffff) {
-        bad = true;  // appends nothing
-        len[i] = max(len[i], 0);
+        bad = bad || len[i] >= 0 || add[i] != 0;  // appends nothing; a padding row that wants nothing is no error
         add[i] = 0;
+      } else {
+        fresh[i] = pages_of(len[i] + add[i]) - pages_of(len[i]);
       }
-      fresh[i] = pages_of(len[i] + add[i]) - pages_of(len[i]);
       nt = add_sat(nt, add[i]);
       np = add_sat(np, fresh[i]);
     }
@@ -175,11 +176,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
   for (int64_t p = gtid; p < all_page; p += gsize) {
     const int b = find_request(page0, a.B, (int)p);
     const int block = pages_of(len_s[b]) + ((int)p - page0[b]);
-    const int page = fresh_page((int)p);
-    if (block < a.max_blocks)
-      a.table[(int64_t)b * a.max_blocks + block] = page;
-    else
+    if (block >= a.max_blocks) {  // past the table: on to the next request's pages
       error = VV_ERR_CAPACITY;
+      if (b + 1 == a.B) break;
+      p += (page0[b + 1] - p - 1) / gsize * gsize;
+      continue;
+    }
+    const int page = fresh_page((int)p);
+    a.table[(int64_t)b * a.max_blocks + block] = page;
     if (page < 0 && error == 0) error = p + cursor >= a.n_free ? VV_ERR_CAPACITY : VV_ERR_RANGE;
   }
   // tokens, four in a row per thread: one bisection, then a walk
@@ -508,8 +512,8 @@ extern "C" vv_status vv_paged_plan(const int32_t* lens, const int32_t* new_lens,
                     page_size, n_free, pages, max_blocks, max_tokens, magic, shift};
   const size_t smem = (size_t)((B + 4) & ~3) * 12;
   VV_CUDA(vv::allow_smem<vv::paged_plan_kernel>((vv::kPlanMaxB + 4) * 12));
-  // one CTA per 2048 tokens, at most one per SM: each repeats the scan, and three per SM measured
-  // 16.4 us where one takes less for 4096 requests with 778k tokens
+  // one CTA per 2048 tokens, at most one per SM, since each repeats the scan: 12.2 us for 4096
+  // requests with 778k tokens, 16.4 us with three per SM
   const int64_t per = vv::kPlanThreads * 4;
   const int grid = (int)std::min<int64_t>(vv::sm_count(), ((int64_t)max_tokens + per - 1) / per);
   vv::paged_plan_kernel<<<grid, vv::kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);

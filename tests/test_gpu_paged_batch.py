@@ -140,6 +140,29 @@ def test_plan_records_errors_and_stays_in_bounds(vv):
     assert p.slots.cpu().tolist() == [-1, 6 * 16 + 15]
 
 
+def test_plan_padding_rows_and_pages_past_a_table(vv):
+    # padding rows at either end and between keep their mark, and take nothing
+    t = i32([[-1, -1], [5, -1], [-1, -1], [6, -1], [-1, -1]])
+    p = vv.vv_paged_plan(i32([-1, 16, -2 ** 31, 15, -7]), i32([0, 1, 0, 2, 0]), t, i32([1, 2, 3]), 16, 8, 5, prefix_len=9)
+    vv.vv_sync_status()
+    assert p.lens.tolist() == [-1, 17, -2 ** 31, 17, -7] and p.offsets.tolist() == [0, 0, 1, 1, 3, 3]
+    assert p.slots.tolist() == [16, 6 * 16 + 15, 32, -1, -1] and p.positions.tolist() == [25, 24, 25, 0, 0]
+    assert t.tolist() == [[-1, -1], [5, 1], [-1, -1], [6, 2], [-1, -1]] and p.cursor.item() == 2
+    # thousands of pages past a table's end, before, between and after requests that fit
+    n = 5000
+    T = [[-1, -1], [-1, 7], [-1, -1], [-1, -1]]
+    p, t = plan_error(vv, vv.VV_ERR_CAPACITY, [0, 0, 0, 0], [n, 1, n, 2], T, np.arange(2 * n + 3) % 8, 1, 8, 2 * n + 3)
+    assert p.cursor.item() == 2 * n + 3
+    assert t.tolist() == [[0, 1], [n % 8, 7], [(n + 1) % 8, (n + 2) % 8], [(2 * n + 1) % 8, (2 * n + 2) % 8]]
+    want = np.full(2 * n + 3, -1)
+    want[[0, 1, n, n + 1, n + 2, 2 * n + 1, 2 * n + 2]] = [0, 1, n % 8, (n + 1) % 8, (n + 2) % 8, (2 * n + 1) % 8, (2 * n + 2) % 8]
+    assert np.array_equal(p.slots.cpu().numpy(), want)
+    # as many as 31 bits hold end as an error, soon
+    big = 2 ** 31 - 1
+    p, t = plan_error(vv, vv.VV_ERR_CAPACITY, [0, 0, 2, 0], [big, 1, big - 2, 0], T, [1, 2, 3, 4], 1, 8, 4)
+    assert t[0].tolist() == [1, 2] and p.slots.tolist() == [1, 2, -1, -1]
+
+
 # ------------------------------------------------------------------------------ rope append
 def pools(vv, pages, hkv, ps, dtype, seed, tokens_first=False):
     shape = (pages, ps, hkv, 128) if tokens_first else (pages, hkv, ps, 128)
