@@ -272,7 +272,8 @@ vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
  * of the same type with the given strides (elements, multiples of 8), e.g. one layer's slice of a
  * decoder's cache (NULL when prefix_len is 0); block_tables device int32 [B, max_blocks], only
  * the entries that own_lens reaches are read; own_lens device int32 [B]; out [B, Hq, D], rows
- * out_stride apart; lse device fp32 [B, Hq] or NULL: log of the sum of exp(score).
+ * out_stride apart (q itself is allowed); lse device fp32 [B, Hq] or NULL: log of the sum of
+ * exp(score).
  * A sequence without any key (or with every score -inf) gives zeros and lse -inf; own_lens[b] < 0
  * marks a padding row: its q is not used and its rows of out and lse are left as they were.
  * Scores, softmax and sums in fp32; the weights are rounded to the element type before they meet

@@ -448,6 +448,48 @@ def test_prefix_attn_workspace_is_left_ready_and_results_repeat(vv):
     attn_check(d, b, lb)
 
 
+@pytest.mark.parametrize("hq,hkv,P", [(9, 1, 20), (22, 2, 300), (16, 1, 128), (13, 1, 127)])
+def test_prefix_attn_wide_groups_and_any_workspace(vv, hq, hkv, P):
+    """9 to 16 query heads per key-value head, on a workspace of NaN; the result may take q's place."""
+    c = attn_case(vv, 4, hq, hkv, P, [70, 0, -1, 17], 16, F16, seed=hq)
+    ws = torch.full((attn_ws(vv, c).numel(),), 0xff, dtype=torch.uint8, device="cuda")
+    out, lse = attn_run(vv, c, ws)
+    vv.vv_sync_status()
+    attn_check(c, out, lse)
+    q = c["q"]
+    c["q"] = q.clone()
+    attn_run(vv, c, ws, out=c["q"])
+    live = [0, 1, 3]
+    assert torch.equal(c["q"][live], out[live]) and torch.equal(c["q"][2], q[2])
+
+
+def test_prefix_attn_two_streams_and_two_threads(vv):
+    """Calls on workspaces of their own may run at once, from two host threads too."""
+    from threading import Thread
+
+    cs = [attn_case(vv, 12, 12, 2, 1500, [40 * i for i in range(12)], 16, F16, seed=1),
+          attn_case(vv, 3, 28, 4, 60, [700, 2, 90], 32, BF16, seed=2)]
+    wss, want = [attn_ws(vv, c) for c in cs], [attn_run(vv, c) for c in cs]
+    tabs = [(i32(c["tables"]), i32(c["lens"])) for c in cs]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        c, s = cs[i], torch.cuda.Stream()
+        for _ in range(20):
+            got[i].append(vv.vv_gqa_prefix_attn(c["q"], c["kpre"], c["vpre"], c["kv"], *tabs[i], c["scale"], wss[i], stream=s))
+        s.synchronize()
+
+    threads = [Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    vv.vv_sync_status()
+    for i in range(2):
+        assert len(got[i]) == 20 and all(torch.equal(o, want[i][0]) for o in got[i])
+
+
 # ---------------------------------------------------------------------------------- logits
 def logits_case(B, V, W, dtype, seed, bias=0, mask=False, penalties=True, prompt=None):
     r = synth.rng(seed)
