@@ -5,7 +5,7 @@
 //   seen:  x <- x > 0 ? x / r : x * r        n > 0: x <- (x - f n) - p
 //   bias:  x <- x + w                        bit 0: x <- -inf
 //
-// One pass over the logits.  A CTA owns a run of kSlice consecutive tokens of one row; it issues
+// One pass over the logits.  A CTA owns a slice of consecutive tokens of one row; it issues
 // the loads of its logits into registers first and, while they are on their way, reads the row's
 // whole history, keeping what falls into its run: one bit per token in shared memory says whether
 // it occurs, and only the counters of generated tokens are ever touched.  Equal ids of a warp are
@@ -29,8 +29,6 @@ namespace vv {
 namespace {
 
 constexpr int kLogitThreads = 256;
-constexpr int kPer = 32;                        // logits per thread, in registers
-constexpr int kSlice = kLogitThreads * kPer;    // 8192 tokens of a row per CTA
 
 struct RowBest {
   unsigned long long key;  // 0: nothing above -inf so far
@@ -79,8 +77,9 @@ __device__ __forceinline__ unsigned load_now(const int32_t* p) {
   return v;
 }
 
-template <typename T>
+template <typename T, int kPer>  // logits per thread, in registers
 __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const __grid_constant__ LogitsArgs a) {
+  constexpr int kSlice = kLogitThreads * kPer;  // tokens of a row per CTA
   constexpr int VEC = 16 / sizeof(T);   // elements of a 16-byte load
   constexpr int NV = kPer / VEC;        // such loads per thread
   extern __shared__ __align__(16) unsigned char lsm[];
@@ -95,7 +94,7 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
   const int bias_shift = a.packed ? 16 : 0;
   const unsigned count_mask = a.packed ? 0xffffu : 0xffffffffu;
   __shared__ __align__(16) unsigned bits[kSlice / 32][4];  // a bit per token: seen, said, has a bias; allowed
-  constexpr int kSeen = 0, kSaid = 1, kBias = 2, kAllowed = 3;
+  constexpr int kSeen = 0, kSaid = 1, kBias = 2;
   const int b = blockIdx.y, v0 = blockIdx.x * kSlice, tid = threadIdx.x;
   const int nv = min(kSlice, a.V - v0);
   const T* in = static_cast<const T*>(a.in) + (int64_t)b * a.in_stride + v0;
@@ -153,8 +152,9 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
       near_val[k] = __uint_as_float(load_now(reinterpret_cast<const int32_t*>(a.r.bias_vals + i)));
     }
   }
-  static_assert(kSlice / 32 == kLogitThreads, "a word of the mask per thread");
-  const int left = nv - tid * 32;
+  static_assert(kSlice / 32 <= kLogitThreads, "at most a word of the mask per thread");
+  const bool has_word = kSlice / 32 == kLogitThreads || tid < kSlice / 32;
+  const int left = has_word ? nv - tid * 32 : 0;
   // tokens past the row's end are barred like masked ones
   unsigned allowed = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0u;
   if (mask && left > 0) allowed &= mask[(v0 >> 5) + tid];
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
   if (bad && tid == 0 && blockIdx.x == 0) set_device_error(VV_ERR_RANGE);
   // which tokens of the run the history and the biases name: one bit each, so that nothing else has
   // to be cleared, and logits without any are only masked and copied
-  *reinterpret_cast<uint4*>(bits[tid]) = make_uint4(0, 0, 0, allowed);
+  if (has_word) *reinterpret_cast<uint4*>(bits[tid]) = make_uint4(0, 0, 0, allowed);
   __syncthreads();
   if (history || biased) {
     // a prompt may hold one id thousands of times: the bit is looked at before it is set
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
   // unchanged where they were read (in place: as the copy just written).
   if (history || biased) {
     __syncthreads();
-    const uint4 word = *reinterpret_cast<const uint4*>(bits[tid]);
+    const uint4 word = has_word ? *reinterpret_cast<const uint4*>(bits[tid]) : make_uint4(0, 0, 0, 0);
     for (unsigned rest = (word.x | word.y | word.z) & word.w; rest; rest &= rest - 1) {
       const unsigned bit = rest & -rest;
       const int d = tid * 32 + __ffs(rest) - 1;
@@ -324,13 +324,23 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
   }
 }
 
+template <typename T, int PER>
+cudaError_t launch_slices(const LogitsArgs& a, int B, cudaStream_t s) {
+  constexpr int kSlice = kLogitThreads * PER;
+  const size_t smem = (a.r.tokens ? kSlice * 4 : 0) + (a.r.bias_ids && !a.packed ? kSlice * 4 : 0);
+  const cudaError_t e = allow_smem<logits_process_kernel<T, PER>>(kSlice * 8);
+  if (e != cudaSuccess) return e;
+  logits_process_kernel<T, PER><<<dim3((a.V + kSlice - 1) / kSlice, B), kLogitThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+// Every CTA reads its row's whole history, so a slice is 8192 tokens; a few rows take slices of 2048
+// while these are at most three CTAs per SM (four fit): with 4785 ids and rows of 152064, 1 / 2 / 4 / 8
+// rows take 8.5 / 10.0 / 9.4 / 10.9 us in large slices and 6.6 / 7.9 / 8.7 / 11.8 us in small ones.
 template <typename T>
 cudaError_t launch_logits(const LogitsArgs& a, int B, cudaStream_t s) {
-  const size_t smem = (a.r.tokens ? kSlice * 4 : 0) + (a.r.bias_ids && !a.packed ? kSlice * 4 : 0);
-  cudaError_t e = allow_smem<logits_process_kernel<T>>(kSlice * 8);
-  if (e != cudaSuccess) return e;
-  logits_process_kernel<T><<<dim3((a.V + kSlice - 1) / kSlice, B), kLogitThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  const int64_t small = (int64_t)B * ((a.V + kLogitThreads * 8 - 1) / (kLogitThreads * 8));
+  return small <= 3 * sm_count() ? launch_slices<T, 8>(a, B, s) : launch_slices<T, 32>(a, B, s);
 }
 
 }  // namespace

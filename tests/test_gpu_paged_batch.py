@@ -580,6 +580,21 @@ def test_logits_process(vv, B, V, W, dtype, bias, mask):
     assert same.data_ptr() == x.data_ptr() and torch.equal(same, out) and torch.equal(idx, idx2)
 
 
+# rows enough for slices of 8192 tokens
+MANY = [(150, 8193, 100, F16, 9, True), (60, 16384, 3000, F32, 200, True), (112, 8192, 64, BF16, 0, True),
+        (45, 20481, 70000, F32, 30, False), (90, 10000, 6000, BF16, 800, True), (230, 2049, 0, F32, 4, False)]
+
+
+@pytest.mark.parametrize("B,V,W,dtype,bias,mask", MANY)
+def test_logits_process_many_rows(vv, B, V, W, dtype, bias, mask):
+    c = logits_case(B, V, W, dtype, V + W, bias, mask)
+    out, idx = logits_run(vv, c)
+    logits_check(c, out, idx)
+    x = c["x"].clone()
+    same, idx2 = logits_run(vv, dict(c, x=x), out=x)  # in place
+    assert torch.equal(same, out) and torch.equal(idx, idx2)
+
+
 def test_logits_process_edges(vv):
     V = 20000
     # nothing but a copy and the greedy token; lowest of a tie, across slices and at -0 / +0
