@@ -15,7 +15,10 @@
 // the order of arrival and picks the lowest token on ties; the last CTA of a row writes it and
 // leaves the workspace zero.
 //
-// Bound by HBM: 8 bytes per logit (fp32), the history and mask are a few per cent.
+// 8 bytes per logit (fp32), history and mask a few per cent: 64 rows of 152064 take 12.4 us at the
+// copy's rate, here 25.8 (3.1 TB/s).  What bounds it is the chain of a CTA (ids and logits, marks,
+// counts, dense pass, named tokens, each behind a barrier) and its instructions, half of them for the
+// 4785 ids of a row, which every slice looks through; one row is a chain of latencies (6.4 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -28,7 +31,6 @@
 namespace vv {
 namespace {
 
-constexpr int kLogitThreads = 256;
 
 struct RowBest {
   unsigned long long key;  // 0: nothing above -inf so far
@@ -77,15 +79,15 @@ __device__ __forceinline__ unsigned load_now(const int32_t* p) {
   return v;
 }
 
-template <typename T, int kPer>  // logits per thread, in registers
-__global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const __grid_constant__ LogitsArgs a) {
-  constexpr int kSlice = kLogitThreads * kPer;  // tokens of a row per CTA
+template <typename T, int kThreads, int kPer>  // kPer: logits per thread, in registers
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logits_process_kernel(const __grid_constant__ LogitsArgs a) {
+  constexpr int kSlice = kThreads * kPer;  // tokens of a row per CTA
   constexpr int VEC = 16 / sizeof(T);   // elements of a 16-byte load
   constexpr int NV = kPer / VEC;        // such loads per thread
   extern __shared__ __align__(16) unsigned char lsm[];
-  __shared__ unsigned long long warp_key[kLogitThreads / 32];
-  constexpr int kNear = 2;  // biases of a thread in registers
-  __shared__ float bias_val[kNear * kLogitThreads];
+  __shared__ unsigned long long warp_key[kThreads / 32];
+  constexpr int kNear = 512 / kThreads;  // biases of a thread in registers
+  __shared__ float bias_val[kNear * kThreads];
   const bool history = a.r.tokens != nullptr, biased = a.r.bias_ids != nullptr;
   // per token of the run: how often it was generated, and which of the row's biases it has; in one
   // word when both fit 16 bits (history and biases of at most 65535 entries)
@@ -112,12 +114,12 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
   const int width = history ? a.r.max_tokens : 0;
   // ids of a thread in registers, 5120 of a row together: one round trip to memory for most rows,
   // and the second pass over them (the counting) needs none
-  constexpr int kMany = 20;
+  constexpr int kMany = 5120 / kThreads;
   unsigned t[kMany];
   auto fetch = [&](int j0) {
 #pragma unroll
     for (int j = 0; j < kMany; ++j) {
-      const int i = j0 + j * kLogitThreads + tid;
+      const int i = j0 + j * kThreads + tid;
       t[j] = (unsigned)v0 - 1u;  // outside the run
       if (i < width) t[j] = load_now(tok + i);
     }
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
   float near_val[kNear];
 #pragma unroll
   for (int k = 0; k < kNear; ++k) {
-    const int i = i0 + k * kLogitThreads + tid;
+    const int i = i0 + k * kThreads + tid;
     near_id[k] = (unsigned)v0 - 1u;  // outside the run
     near_val[k] = 0.f;
     if (i < i1) {
@@ -152,22 +154,24 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
       near_val[k] = __uint_as_float(load_now(reinterpret_cast<const int32_t*>(a.r.bias_vals + i)));
     }
   }
-  static_assert(kSlice / 32 <= kLogitThreads, "at most a word of the mask per thread");
-  const bool has_word = kSlice / 32 == kLogitThreads || tid < kSlice / 32;
+  static_assert(kSlice / 32 <= kThreads, "at most a word of the mask per thread");
+  const bool has_word = kSlice / 32 == kThreads || tid < kSlice / 32;
   const int left = has_word ? nv - tid * 32 : 0;
   // tokens past the row's end are barred like masked ones
   unsigned allowed = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0u;
   if (mask && left > 0) allowed &= mask[(v0 >> 5) + tid];
-  const bool whole = wide && nv == kSlice;
+  const bool vec = wide && nv % VEC == 0;
   __align__(16) T x[kPer];
-  if (whole) {
+  if (vec) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      *reinterpret_cast<uint4*>(&x[j * VEC]) = *reinterpret_cast<const uint4*>(in + (j * kLogitThreads + tid) * VEC);
+    for (int j = 0; j < NV; ++j) {
+      const int e0 = (j * kThreads + tid) * VEC;
+      *reinterpret_cast<uint4*>(&x[j * VEC]) = e0 < nv ? *reinterpret_cast<const uint4*>(in + e0) : make_uint4(0, 0, 0, 0);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e0 = (j * kLogitThreads + tid) * VEC;
+      const int e0 = (j * kThreads + tid) * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) x[j * VEC + e] = e0 + e < nv ? in[e0 + e] : from_f32<T>(0.f);
     }
@@ -184,17 +188,22 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
       volatile unsigned* word = &bits[d >> 5][which];
       if (!((*word >> (d & 31)) & 1)) atomicOr(&bits[d >> 5][which], 1u << (d & 31));
     };
-    constexpr int kRound = kMany * kLogitThreads;
+    constexpr int kGroup = kMany % 4 == 0 ? 4 : 5;
+    static_assert(kMany % kGroup == 0, "whole groups");
+    constexpr int kRound = kMany * kThreads;
     for (int j0 = 0; j0 < len; j0 += kRound) {
       if (j0 > 0) fetch(j0);
 #pragma unroll
-      for (int g = 0; g < kMany; g += 4) {
-        if (j0 + g * kLogitThreads >= len) break;
-        // mostly none of the four falls into the run
-        if (min(min(t[g], t[g + 1]), min(t[g + 2], t[g + 3])) >= (unsigned)nv) continue;
+      for (int g = 0; g < kMany; g += kGroup) {
+        if (j0 + g * kThreads >= len) break;
+        // mostly none of the group falls into the run
+        unsigned least = t[g];
 #pragma unroll
-        for (int j = g; j < g + 4; ++j) {
-          const int i = j0 + j * kLogitThreads + tid;
+        for (int j = g + 1; j < g + kGroup; ++j) least = min(least, t[j]);
+        if (least >= (unsigned)nv) continue;
+#pragma unroll
+        for (int j = g; j < g + kGroup; ++j) {
+          const int i = j0 + j * kThreads + tid;
           if (t[j] >= (unsigned)nv || i >= len) continue;
           if (i < plen) {
             mark(kSeen, t[j]);
@@ -210,15 +219,15 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
 #pragma unroll
       for (int k = 0; k < kNear; ++k) {
         const unsigned d = near_id[k] - (unsigned)v0;
-        if (d < (unsigned)nv) f(k * kLogitThreads + tid, d);
+        if (d < (unsigned)nv) f(k * kThreads + tid, d);
       }
-      for (int i = i0 + kNear * kLogitThreads + tid; i < i1; i += kLogitThreads) {
+      for (int i = i0 + kNear * kThreads + tid; i < i1; i += kThreads) {
         const unsigned d = (unsigned)a.r.bias_ids[i] - (unsigned)v0;
         if (d < (unsigned)nv) f(i - i0, d);
       }
     };
 #pragma unroll
-    for (int k = 0; k < kNear; ++k) bias_val[k * kLogitThreads + tid] = near_val[k];
+    for (int k = 0; k < kNear; ++k) bias_val[k * kThreads + tid] = near_val[k];
     each_bias([&](int, unsigned d) {
       mark(kBias, d);
       bias[d] = 0;
@@ -231,8 +240,8 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
       if (len > kRound) fetch(j0);
 #pragma unroll
       for (int j = 0; j < kMany; ++j) {
-        if (j0 + (j + 1) * kLogitThreads <= plen || j0 + j * kLogitThreads >= len) continue;  // the prompt's, or none
-        const int i = j0 + j * kLogitThreads + tid;
+        if (j0 + (j + 1) * kThreads <= plen || j0 + j * kThreads >= len) continue;  // the prompt's, or none
+        const int i = j0 + j * kThreads + tid;
         const unsigned d = t[j] < (unsigned)nv && i >= plen && i < len ? t[j] : 0xffffffffu;
         if (!__any_sync(0xffffffffu, d != 0xffffffffu)) continue;
         const unsigned same = __match_any_sync(0xffffffffu, d);
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
   constexpr unsigned kAll = (1u << VEC) - 1;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e0 = (j * kLogitThreads + tid) * VEC;  // its VEC (4 or 8) bits lie in one word
+    const int e0 = (j * kThreads + tid) * VEC;  // its VEC (4 or 8) bits lie in one word
     const uint4 word = *reinterpret_cast<const uint4*>(bits[e0 >> 5]);
     const unsigned named = (word.x | word.y | word.z) >> (e0 & 31), barred = ~(word.w >> (e0 & 31));
     float y[VEC];
@@ -262,8 +271,8 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
         if (((named | barred) >> e) & 1) y[e] = -INFINITY;
       }
     }
-    if (whole) {
-      *reinterpret_cast<uint4*>(out + e0) = *reinterpret_cast<const uint4*>(&x[j * VEC]);
+    if (vec) {
+      if (e0 < nv) *reinterpret_cast<uint4*>(out + e0) = *reinterpret_cast<const uint4*>(&x[j * VEC]);
     } else {
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
@@ -292,7 +301,7 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
       if (word.y & bit) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)(count[d] & count_mask))), pres);
       if (word.z & bit) {
         const unsigned k = bias[d] >> bias_shift;
-        y = __fadd_rn(y, k < kNear * kLogitThreads ? bias_val[k] : a.r.bias_vals[i0 + k]);
+        y = __fadd_rn(y, k < kNear * kThreads ? bias_val[k] : a.r.bias_vals[i0 + k]);
       }
       out[d] = from_f32<T>(y);
       if (y > best || (y == best && v0 + d < best_at)) {
@@ -310,7 +319,7 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
   if ((tid & 31) == 0) warp_key[tid >> 5] = key;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < kLogitThreads / 32; ++w) key = warp_key[w] > key ? warp_key[w] : key;
+    for (int w = 1; w < kThreads / 32; ++w) key = warp_key[w] > key ? warp_key[w] : key;
     RowBest* row = a.ws + b;
     if (gridDim.x > 1) {
       if (key) atomicMax(&row->key, key);
@@ -324,23 +333,25 @@ __global__ void __launch_bounds__(kLogitThreads, 4) logits_process_kernel(const 
   }
 }
 
-template <typename T, int PER>
+template <typename T, int THREADS, int PER>
 cudaError_t launch_slices(const LogitsArgs& a, int B, cudaStream_t s) {
-  constexpr int kSlice = kLogitThreads * PER;
+  constexpr int kSlice = THREADS * PER;
   const size_t smem = (a.r.tokens ? kSlice * 4 : 0) + (a.r.bias_ids && !a.packed ? kSlice * 4 : 0);
-  const cudaError_t e = allow_smem<logits_process_kernel<T, PER>>(kSlice * 8);
+  const cudaError_t e = allow_smem<logits_process_kernel<T, THREADS, PER>>(kSlice * 8);
   if (e != cudaSuccess) return e;
-  logits_process_kernel<T, PER><<<dim3((a.V + kSlice - 1) / kSlice, B), kLogitThreads, smem, s>>>(a);
+  logits_process_kernel<T, THREADS, PER><<<dim3((a.V + kSlice - 1) / kSlice, B), THREADS, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-// Every CTA reads its row's whole history, so a slice is 8192 tokens; a few rows take slices of 2048
-// while these are at most three CTAs per SM (four fit): with 4785 ids and rows of 152064, 1 / 2 / 4 / 8
-// rows take 8.5 / 10.0 / 9.4 / 10.9 us in large slices and 6.6 / 7.9 / 8.7 / 11.8 us in small ones.
+// Every CTA reads its row's whole history, so a slice is 12288 tokens (64 rows of 152064 with 4785
+// ids: 25.8 us; slices of 8192 / 4096 / 16384 tokens: 26.9-29.8 / 38 / 25.4 us, eight rows 8.9 / 9.5 / 10.3
+// where these take 9.2); a few rows take slices of 2048 while these are at
+// most two CTAs per SM: 1 / 2 / 4 / 8 such rows take 7.5 / 9.1 / 8.4 / 10.0 us in large slices and 6.6 /
+// 8.3 / 8.6 / 11.6 us in small ones.
 template <typename T>
 cudaError_t launch_logits(const LogitsArgs& a, int B, cudaStream_t s) {
-  const int64_t small = (int64_t)B * ((a.V + kLogitThreads * 8 - 1) / (kLogitThreads * 8));
-  return small <= 3 * sm_count() ? launch_slices<T, 8>(a, B, s) : launch_slices<T, 32>(a, B, s);
+  const int64_t small = (int64_t)B * ((a.V + 2047) / 2048);
+  return small <= 2 * sm_count() ? launch_slices<T, 256, 8>(a, B, s) : launch_slices<T, 512, 24>(a, B, s);
 }
 
 }  // namespace

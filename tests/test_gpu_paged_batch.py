@@ -580,8 +580,8 @@ def test_logits_process(vv, B, V, W, dtype, bias, mask):
     assert same.data_ptr() == x.data_ptr() and torch.equal(same, out) and torch.equal(idx, idx2)
 
 
-# rows enough for slices of 8192 tokens
-MANY = [(150, 8193, 100, F16, 9, True), (60, 16384, 3000, F32, 200, True), (112, 8192, 64, BF16, 0, True),
+# rows enough for the larger slices
+MANY = [(40, 28672, 50, F16, 3, True), (150, 8193, 100, F16, 9, True), (60, 16384, 3000, F32, 200, True), (112, 8192, 64, BF16, 0, True),
         (45, 20481, 70000, F32, 30, False), (90, 10000, 6000, BF16, 800, True), (230, 2049, 0, F32, 4, False)]
 
 
