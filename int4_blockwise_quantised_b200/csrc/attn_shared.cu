@@ -10,8 +10,12 @@
 // L = sum l_i e^(m_i - M), O = sum o_i e^(m_i - M).  So three kernels, each launched while the one
 // before it still runs (programmatic launch): the sequences' own pages, the shared prompt for all
 // sequences together (attn_shared_tc.cu, nothing to do with the first; it ends after it), and the
-// join of all parts, a warp per output row.  Joining at the end of the first two took longer: a few
-// CTAs hold several heads, and a head's parts are a dozen dependent reads.
+// join of all parts, a warp per output row.  Joining at the end of the first two took longer (17.4 us
+// for 16 sequences on a prompt of 4530, 12.8 with the join apart): a few CTAs hold several heads, and a
+// head's parts are a dozen dependent reads.
+//
+// Measured: 2 x (1024 + at most 64) keys, 12 / 2 heads: 8.6 us; 16 x (4530 + 257): 12.7 us; 48 x (32768 +
+// 1024), 28 / 4 heads: 46 us (23 GFLOP, 125 MB); 23 x 4785 without a prompt: 23.6 us (92 MB, 3.9 TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
