@@ -253,23 +253,24 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 //   (x_i, x_{i+64}) <- (x_i c - x_{i+64} s, x_{i+64} c + x_i s),  angle = pos * theta^(-2i/128)
 //
 // Bound by HBM: every head row is read once and written once (512 bytes for 128 elements): 50001
-// tokens of 28 + 4 + 4 heads take 155 us (5.9 TB/s); with norms the instructions count too, 4530 such
-// tokens take 24 us (3.5 TB/s, 42% of the issue slots), and 16 tokens of 12 + 2 + 2 heads 3.4 us.  A unit is one token's heads, or a part of them; a warp works alone
-// on its units and has the next one or two on their way (cp.async.bulk into a ring of its own, a
-// token's heads of one kind are contiguous), whatever its registers and without a barrier between
-// warps.  Half a warp turns one head row, 16 bytes a lane; the rotation's
-// partner is read from shared memory too.  A token's angles are found once per unit, two a lane: the
-// turns pos * theta^(-2i/128) / 2 pi reduced to [-1/2, 1/2] in 64 bits (in 32 bits a position of
-// 10^6 would lose the angle's second digit), then sine and cosine of the remainder in 32 bits.
+// tokens of 28 + 4 + 4 heads take 153 us (6.0 TB/s); with norms the instructions count too, 158 us and
+// 21.7 us for 4530 such tokens (3.8 TB/s); 16 tokens of 12 + 2 + 2 heads take 2.9 us.
+// A unit is one token's heads, or a part of them; a warp works alone on its units and has the next
+// one or two on their way (cp.async.bulk into a ring of its own, a token's heads of one kind are
+// contiguous), whatever its registers and without a barrier between warps.  Half a warp turns one
+// head row; a lane holds four elements and their partners, so that each is read and converted once.
+// A token's angles are found once per unit, two a lane: the turns pos * theta^(-2i/128) / 2 pi
+// reduced to [-1/2, 1/2] in 64 bits (in 32 bits a position of 10^6 would lose the angle's second
+// digit), then sine and cosine of the remainder in 32 bits.
 constexpr int kHeadDim = 128;
 constexpr int kRopeHeads = 18;  // most heads of a unit, 4.5 KB
-// With norms a row takes twice the instructions: eight warps per CTA (two CTAs per SM) and one unit on
-// its way beside the one in work.  Without, as many warps ask memory for more than it gives in
-// good order: 50001 tokens of 28 + 4 + 4 heads take 172 us with eight and 156 with six (150 with
-// the slower loop that handled all rows alike); with norms 181 and 208.
+// With norms a row takes half as many instructions again: eight warps per CTA (two CTAs per SM) and one
+// unit on its way beside the one in work.  Without, as many warps ask memory for more than it gives
+// in good order: 50001 tokens of 28 + 4 + 4 heads take 169 us with eight, 170 with six, 153 with five
+// and 160 with four; with norms 158 with eight and 225 with five.
 template <bool GAINS>
 struct RopeShape {
-  static constexpr int kWarps = GAINS ? 8 : 6;
+  static constexpr int kWarps = GAINS ? 8 : 5;
   static constexpr int kStages = GAINS ? 2 : 3;
 };
 
@@ -304,16 +305,40 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
+__device__ __forceinline__ uint32_t pack2(float2 x);
 template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint32_t pack2<__half>(float2 x) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float2 x) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two fp32 numbers in one register pair: sm_100 multiplies and adds both in one instruction.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 pair(float2 x) { return pair(x.x, x.y); }
+__device__ __forceinline__ float2 unpair(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 template <typename T, bool GAINS>
@@ -352,8 +377,7 @@ __global__ void __launch_bounds__(RopeShape<GAINS>::kWarps * 32, 2)
 #pragma unroll
   for (int i = 0; i < kRopeStages; ++i) copy(u0 + i * step, i);
 
-  const int c = lane & 15;  // 16-byte piece of the row
-  const float sign = c < 8 ? -1.f : 1.f;
+  const int c = lane & 15;  // elements 4c .. 4c + 3 of a row and their partners; 16-byte piece of a value row
   const double f0 = a.turns[lane], f1 = a.turns[lane + 32];
   int pos = 0;
   int64_t slot = -1;
@@ -385,56 +409,62 @@ __global__ void __launch_bounds__(RopeShape<GAINS>::kWarps * 32, 2)
       slot = a.slots[(u + step) / a.parts];
     }
     __syncwarp();
-    // y = x * own + partner * other, pairs of elements: the cosines and sines times the gains
-    float2 own[4], other[4];
+    // (x, y) <- (x cx + y sx, y cy + x sy): the cosines and sines times the gains, two pairs a word
+    f32x2 cx[2], sx[2], cy[2], sy[2];
     auto factors = [&](const void* gain) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 f = *reinterpret_cast<const float4*>(&cs[(c & 7) * 8 + 2 * j]);
-        own[j] = make_float2(f.x, f.z);
-        other[j] = make_float2(f.y * sign, f.w * sign);
+      for (int j = 0; j < 2; ++j) {
+        const float4 f = *reinterpret_cast<const float4*>(&cs[c * 4 + 2 * j]);
+        float2 g = make_float2(1.f, 1.f), h = g;
         if (GAINS && gain) {
-          const float2 g = unpack2<T>(static_cast<const uint32_t*>(gain)[c * 4 + j]);
-          const float2 h = unpack2<T>(static_cast<const uint32_t*>(gain)[(c ^ 8) * 4 + j]);
-          own[j] = make_float2(own[j].x * g.x, own[j].y * g.y);
-          other[j] = make_float2(other[j].x * h.x, other[j].y * h.y);
+          g = unpack2<T>(static_cast<const uint32_t*>(gain)[c * 2 + j]);
+          h = unpack2<T>(static_cast<const uint32_t*>(gain)[32 + c * 2 + j]);
         }
+        cx[j] = pair(f.x * g.x, f.z * g.y);
+        sx[j] = pair(-f.y * h.x, -f.w * h.y);
+        cy[j] = pair(f.x * h.x, f.z * h.y);
+        sy[j] = pair(f.y * g.x, f.w * g.y);
       }
     };
     // rows from .. to - 1 of the unit, two at a time, row r to dst(r)
+    // (two iterations at once send memory the same requests in bursts: 157 us instead of 153)
     auto turn = [&](int from, int to, bool norm, auto&& dst) {
-      const unsigned char* in = ring + st * unit_bytes + c * 16;
-      const int swap = (c < 8 ? 8 : -8) * 16;
-#pragma unroll 4
+      const unsigned char* in = ring + st * unit_bytes + c * 8;
+#pragma unroll 1
       for (int r0 = from; r0 < to; r0 += 2) {
         const int r = min(r0 + (lane >> 4), to - 1);  // an odd last row is done twice
-        const uint4 xw = *reinterpret_cast<const uint4*>(in + r * kRow);
-        const uint4 pw = *reinterpret_cast<const uint4*>(in + r * kRow + swap);
-        float2 x[4] = {unpack2<T>(xw.x), unpack2<T>(xw.y), unpack2<T>(xw.z), unpack2<T>(xw.w)};
-        const float2 p[4] = {unpack2<T>(pw.x), unpack2<T>(pw.y), unpack2<T>(pw.z), unpack2<T>(pw.w)};
-        float inv = 1.f;
-        if (GAINS && norm) {
-          float ss = 0.f;
+        const uint2 xw = *reinterpret_cast<const uint2*>(in + r * kRow);
+        const uint2 yw = *reinterpret_cast<const uint2*>(in + r * kRow + kRow / 2);
+        const f32x2 x[2] = {pair(unpack2<T>(xw.x)), pair(unpack2<T>(xw.y))};
+        const f32x2 y[2] = {pair(unpack2<T>(yw.x)), pair(unpack2<T>(yw.y))};
+        f32x2 u[2], v[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) ss = fmaf(x[j].x, x[j].x, fmaf(x[j].y, x[j].y, ss));
+        for (int j = 0; j < 2; ++j) {
+          u[j] = fma2(x[j], cx[j], mul2(y[j], sx[j]));
+          v[j] = fma2(y[j], cy[j], mul2(x[j], sy[j]));
+        }
+        if (GAINS && norm) {
+          const float2 s2 = unpair(fma2(y[1], y[1], fma2(y[0], y[0], fma2(x[1], x[1], mul2(x[0], x[0])))));
+          float ss = s2.x + s2.y;
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          inv = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
-        }
+          const float inv = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j].x = fmaf(x[j].x, own[j].x, p[j].x * other[j].x) * inv;
-          x[j].y = fmaf(x[j].y, own[j].y, p[j].y * other[j].y) * inv;
+          for (int j = 0; j < 2; ++j) {
+            u[j] = mul2(u[j], pair(inv, inv));
+            v[j] = mul2(v[j], pair(inv, inv));
+          }
         }
-        *reinterpret_cast<uint4*>(dst(r)) = make_uint4(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y),
-                                                                pack2<T>(x[2].x, x[2].y), pack2<T>(x[3].x, x[3].y));
+        char* to_row = dst(r);
+        *reinterpret_cast<uint2*>(to_row) = make_uint2(pack2<T>(unpair(u[0])), pack2<T>(unpair(u[1])));
+        *reinterpret_cast<uint2*>(to_row + kRow / 2) = make_uint2(pack2<T>(unpair(v[0])), pack2<T>(unpair(v[1])));
       }
     };
     const int q_end = min(max(a.Hq - h0, 0), nh), k_end = min(max(a.Hq + a.Hkv - h0, 0), nh);
     if (q_end > 0 || (k_end > 0 && at >= 0)) factors(q_end > 0 ? a.q_gain : a.k_gain);
     wait_phase(&full[st], round & 1);
-    char* q_out = a.q_out + t * a.qo_stride + h0 * kRow + c * 16;
-    char* k_out = a.kp + at + (h0 - a.Hq) * a.head_stride + c * 16;
+    char* q_out = a.q_out + t * a.qo_stride + h0 * kRow + c * 8;
+    char* k_out = a.kp + at + (h0 - a.Hq) * a.head_stride + c * 8;
     if (!GAINS && at >= 0) {
       // the same factors for queries and keys: one loop
       turn(0, k_end, false, [&](int r) { return r < q_end ? q_out + r * kRow : k_out + r * a.head_stride; });
