@@ -253,8 +253,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 //   (x_i, x_{i+64}) <- (x_i c - x_{i+64} s, x_{i+64} c + x_i s),  angle = pos * theta^(-2i/128)
 //
 // Bound by HBM: every head row is read once and written once (512 bytes for 128 elements): 50001
-// tokens of 28 + 4 + 4 heads take 153 us (6.0 TB/s); with norms the instructions count too, 158 us and
-// 21.7 us for 4530 such tokens (3.8 TB/s); 16 tokens of 12 + 2 + 2 heads take 2.9 us.
+// tokens of 28 + 4 + 4 heads take 153 to 166 us (6.0 to 5.6 TB/s, by where the tensors lie); with
+// norms the instructions count too, 158 us and 21.7 us for 4530 such tokens (3.8 TB/s); 16 tokens of
+// 12 + 2 + 2 heads take 2.9 us.
 // A unit is one token's heads, or a part of them; a warp works alone on its units and has the next
 // one or two on their way (cp.async.bulk into a ring of its own, a token's heads of one kind are
 // contiguous), whatever its registers and without a barrier between warps.  Half a warp turns one
