@@ -226,8 +226,8 @@ typedef struct vv_paged_kv {
  * 0); cursor device int32 [1] or NULL (0); block_tables device int32 [B, max_blocks]; lens_out
  * device int32 [B]; offsets device int32 [B + 1]; slots device int64 [max_tokens]; positions
  * device int32 [max_tokens]; cursor_out device int32 [1].  Pages are numbers in [0, pages).
- * lens_out and cursor_out must not overlap lens, new_lens and cursor.  page_size >= 1 (any),
- * 1 <= B <= 16384.
+ * No output (block_tables among them) may overlap an input or another output.  page_size >= 1
+ * (any), 1 <= B <= 16384.
  * On the device: any other negative length, one whose position would pass 2^31 - 1, or a page
  * number outside [0, pages) records VV_ERR_RANGE; more new tokens than max_tokens, more pages than
  * free_pages holds or a table longer than max_blocks records VV_ERR_CAPACITY (vv_sync_status

@@ -522,15 +522,24 @@ extern "C" vv_status vv_paged_plan(const int32_t* lens, const int32_t* new_lens,
                      max_tokens <= 0x7ffffff0,
                  "vv_paged_plan: prefix_len=%d n_free=%d max_blocks=%d max_tokens=%d", prefix_len,
                  n_free, max_blocks, max_tokens);
-  // every CTA reads lens, new_lens and cursor while others write the outputs
-  auto apart = [](const void* a, size_t na, const void* b, size_t nb) {
-    const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
-    return x + na <= y || y + nb <= x;
+  // every CTA reads the inputs for itself while others already write the outputs
+  struct Span {
+    const void* at;
+    size_t bytes;
+    bool meets(const Span& o) const {
+      const char *x = static_cast<const char*>(at), *y = static_cast<const char*>(o.at);
+      return x && y && x < y + o.bytes && y < x + bytes;
+    }
   };
-  const size_t nb = (size_t)B * 4;
-  VV_CHECK_ARG(apart(lens, nb, lens_out, nb) && apart(new_lens, nb, lens_out, nb) &&
-                   (!cursor || apart(cursor, 4, cursor_out, 4)),
-               "vv_paged_plan: lens_out and cursor_out must not overlap lens, new_lens and cursor");
+  const size_t nb = (size_t)B * 4, nt = (size_t)max_tokens;
+  const Span in[] = {{lens, nb}, {new_lens, nb}, {free_pages, (size_t)n_free * 4}, {cursor, 4}};
+  const Span outs[] = {{block_tables, nb * max_blocks}, {lens_out, nb},   {offsets, nb + 4},
+                       {slots, nt * 8},                 {positions, nt * 4}, {cursor_out, 4}};
+  for (const Span& o : outs) {
+    for (const Span& i : in)
+      VV_CHECK_ARG(!o.meets(i), "vv_paged_plan: an output overlaps lens, new_lens, free_pages or cursor");
+    for (const Span* p = outs; p != &o; ++p) VV_CHECK_ARG(!o.meets(*p), "vv_paged_plan: two outputs overlap");
+  }
   // division by page_size as a product: with l = ceil(log2 page_size), m = floor(2^(31 + l) / page_size)
   // + 1 is off by less than 2^l / 2^(31 + l) relative, too little to matter below 2^31
   unsigned magic = 0;
