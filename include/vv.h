@@ -279,8 +279,9 @@ vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
  * Scores, softmax and sums in fp32; the weights are rounded to the element type before they meet
  * V (as 2^x of at most 2^8: a relative half step each).
  * ws: device workspace of vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, D, prefix_len,
- * max_blocks * page_size) bytes, 16-byte aligned, of any contents; calls sharing one ws (captured
- * ones included) must not overlap on the GPU.
+ * max_blocks * page_size) bytes, 16-byte aligned, of any contents; one sized for the largest batch,
+ * prompt and table serves all smaller ones of the same heads; calls sharing one ws (captured ones
+ * included) must not overlap on the GPU.
  * Requirements: D == 128, Hq % Hkv == 0, Hq / Hkv <= 16, 1 <= B <= 65535, 1 <= Hkv <= 1024,
  * 0 <= prefix_len < 2^24, max_blocks >= 1, scale positive and finite, 16-byte aligned pointers.
  * On the device, a page number outside [0, pages) records VV_ERR_RANGE and its keys are left

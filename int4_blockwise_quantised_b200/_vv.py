@@ -360,8 +360,8 @@ def vv_gqa_prefix_attn(q, k_prefix, v_prefix, kv, block_tables, lens, scale, ws,
 
     q [B, Hq, 128] (rows may be strided); k_prefix, v_prefix [Hkv, P, 128] or None; kv a PagedKV;
     block_tables int32 [B, max_blocks]; lens int32 [B] (tokens in the pages; < 0: padding row);
-    ws: vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, 128, P, max_blocks * page_size) bytes, of any
-    contents.  Returns out [B, Hq, 128]; lse fp32 [B, Hq] receives the log sums."""
+    ws: vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, 128, P, max_blocks * page_size) bytes (or those of
+    a larger B, P and table with the same heads), of any contents.  Returns out [B, Hq, 128]; lse fp32 [B, Hq] receives the log sums."""
     args = (q, k_prefix, v_prefix, *kv._call, block_tables, lens, scale, ws, out, lse)
     if stream is None:
         return _marshal.gqa_prefix_attn(*args)

@@ -506,20 +506,37 @@ struct Plan {
   int ctas, pre_splits, pre_per;
   size_t run_part, part, pre_part, total;  // byte offsets in the workspace; `where` comes first
 };
-Plan plan_of(int B, int Hkv, int G, int P, int64_t max_own) {
-  Plan p = {};
-  // One sequence shares nothing, and a prompt of a few chunks costs less to read again than a
-  // second kernel: there the prompt's keys are the first chunks of every sequence.
-  const bool shared = B > 1 && P >= kMinShared;
-  if (shared) prefix_tc_split(B * G, Hkv, P, &p.pre_splits, &p.pre_per);
-  const int64_t chunks = (max_own + kChunk - 1) / kChunk + (shared ? 0 : (P + kChunk - 1) / kChunk);
-  p.ctas = (int)std::min<int64_t>(sm_count(), std::max<int64_t>(chunks, 1) * B * Hkv);
-  const size_t set = (size_t)G * kPartRow * sizeof(float), heads = (size_t)B * Hkv;
+// Chunks of a sequence and key-value head: own pages (no more than a length can name) and P prompt keys.
+int64_t chunk_count(int64_t max_own, int P) {
+  const int64_t own = std::min<int64_t>(max_own, int64_t(1) << 31);
+  return std::max<int64_t>((own + kChunk - 1) / kChunk + (P + kChunk - 1) / kChunk, 1);
+}
+void lay_out(Plan& p, int B, int Hkv, int G, int64_t chunks, int64_t pre_rows) {
+  const size_t row = kPartRow * sizeof(float), set = G * row, heads = (size_t)B * Hkv;
+  p.ctas = (int)std::min<int64_t>(sm_count(), chunks * B * Hkv);
   p.run_part = (heads * sizeof(int2) + 255) / 256 * 256;
   p.part = p.run_part + p.ctas * 2 * set;
   p.pre_part = p.part + heads * set;
-  p.total = p.pre_part + p.pre_splits * heads * set;
+  p.total = p.pre_part + pre_rows * row;
+}
+// One sequence shares nothing, and a prompt of a few chunks costs less to read again than a
+// second kernel: there the prompt's keys are the first chunks of every sequence.
+bool prompt_apart(int B, int P) { return B > 1 && P >= kMinShared; }
+Plan plan_of(int B, int Hkv, int G, int P, int64_t max_own) {
+  Plan p = {};
+  const bool shared = prompt_apart(B, P);
+  if (shared) prefix_tc_split(B * G, Hkv, P, &p.pre_splits, &p.pre_per);
+  lay_out(p, B, Hkv, G, chunk_count(max_own, shared ? 0 : P), (int64_t)p.pre_splits * B * Hkv * G);
   return p;
+}
+// What no plan of at most B sequences, P prompt keys and max_own keys of their own exceeds.  A plan's
+// own need is not enough for that: the prompt is cut into fewer parts as the rows of queries grow
+// (28 / 4 heads on 32768 keys: 37 parts for 18 sequences, 12 for 48), and into 31 for 3968 keys
+// where it is 16 for 4096.
+size_t most_bytes(int B, int Hkv, int G, int P, int64_t max_own) {
+  Plan p = {};
+  lay_out(p, B, Hkv, G, chunk_count(max_own, P), prompt_apart(B, P) ? prefix_tc_most_rows(B * G, Hkv, P) : 0);
+  return p.total;
 }
 
 // Tensor map of rows of D elements, the two halves of a row as a dimension of their own so that
@@ -574,7 +591,7 @@ bool sizes_ok(int B, int Hq, int Hkv, int D_, int P) {
 extern "C" size_t vv_gqa_prefix_attn_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t D_,
                                                     int32_t prefix_len, int64_t max_own) {
   if (!vv::sizes_ok(B, Hq, Hkv, D_, prefix_len) || max_own < 0) return 0;
-  return vv::plan_of(B, Hkv, Hq / Hkv, prefix_len, max_own).total;
+  return vv::most_bytes(B, Hkv, Hq / Hkv, prefix_len, max_own);
 }
 
 extern "C" vv_status vv_gqa_prefix_attn(const void* q, int64_t q_stride, int32_t B, int32_t Hq,

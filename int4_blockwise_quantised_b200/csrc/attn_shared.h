@@ -23,6 +23,8 @@ struct PrefixTcArgs {
 };
 // Parts of the prompt's keys (and 128-key blocks per part) for `rows` rows per key-value head.
 void prefix_tc_split(int rows, int Hkv, int P, int* splits, int* per);
+// Upper bound of splits x rows x Hkv over all smaller numbers of rows and prompts.
+int64_t prefix_tc_most_rows(int rows, int Hkv, int P);
 cudaError_t launch_prefix_tc(const PrefixTcArgs& a, cudaStream_t s);
 
 }  // namespace vv

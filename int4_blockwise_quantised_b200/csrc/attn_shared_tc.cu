@@ -372,6 +372,9 @@ cudaError_t launch_t(const KvMaps& mp, const PrefixTcArgs& a, cudaStream_t s) {
   return launch(prefix_tc_kernel<T>, grid, dim3(kThreads), kSmem, s, true, mp, a);
 }
 
+// Most parts that the keys are cut into: enough for a CTA per SM, and at least 8.
+int64_t most_splits(int64_t tiles) { return std::max<int64_t>(8, sm_count() / tiles); }
+
 }  // namespace
 
 void prefix_tc_split(int rows, int Hkv, int P, int* splits, int* per) {
@@ -380,7 +383,7 @@ void prefix_tc_split(int rows, int Hkv, int P, int* splits, int* per) {
   const int64_t tiles = (int64_t)((rows + BM - 1) / BM) * Hkv, sms = sm_count();
   const int blocks = (P + BN - 1) / BN;
   int64_t best = INT64_MAX;
-  const int most = (int)std::min<int64_t>(blocks, std::max<int64_t>(8, sms / tiles));
+  const int most = (int)std::min<int64_t>(blocks, most_splits(tiles));
   for (int s = 1; s <= most; ++s) {
     const int p = (blocks + s - 1) / s, used = (blocks + p - 1) / p;
     const int64_t cost = (tiles * used + sms - 1) / sms * (p + 4) + used / 32;
@@ -390,6 +393,15 @@ void prefix_tc_split(int rows, int Hkv, int P, int* splits, int* per) {
       *per = p;
     }
   }
+}
+
+int64_t prefix_tc_most_rows(int rows, int Hkv, int P) {
+  // The parts fall as the tiles grow, so the most rows of parts are those of some number of full tiles.
+  const int64_t blocks = (P + BN - 1) / BN;
+  int64_t most = 0;
+  for (int64_t t = 1; t <= (rows + BM - 1) / BM; ++t)
+    most = std::max(most, std::min<int64_t>(rows, t * BM) * std::min(blocks, most_splits(t * Hkv)));
+  return most * Hkv;
 }
 
 cudaError_t launch_prefix_tc(const PrefixTcArgs& a, cudaStream_t s) {
