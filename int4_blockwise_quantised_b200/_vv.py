@@ -146,12 +146,24 @@ def _load():
 
 
 lib = _load()
+
+
+class _NoMarshal:
+    """In _marshal's place where it is not built or does not load: the operators that need it say so."""
+
+    def __init__(self, error):
+        self.error = error
+
+    def __getattr__(self, name):
+        raise ImportError(f"vv_{name} needs the extension module _marshal, which is missing or does not load "
+                          f"({self.error}): build it with `python -m int4_blockwise_quantised_b200.build`")
+
+
 try:
     from . import _marshal
-except ImportError as e:
-    raise ImportError("_marshal.so is missing or does not load: build it with `python -m "
-                      "int4_blockwise_quantised_b200.build`") from e
-_marshal.set_error(VVError)
+    _marshal.set_error(VVError)
+except ImportError as e:  # the other operators need libvv.so alone
+    _marshal = _NoMarshal(e)
 
 
 def header_functions(path=HEADER_PATH):

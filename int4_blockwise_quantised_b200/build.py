@@ -1,11 +1,13 @@
 """Build libvv.so in-tree with nvcc for sm_100a (B200).
 
-    python -m int4_blockwise_quantised_b200.build [--force] [-j N]
+    python -m int4_blockwise_quantised_b200.build [--force] [-j N] [--lib-only]
 
 Each csrc/*.cu compiles to an object under _build/ (in parallel, skipped when up to date), then
 all objects link into int4_blockwise_quantised_b200/libvv.so with the CUDA runtime linked
 statically.  csrc/marshal.cpp (tensor arguments of the batch operators) compiles with the host
-compiler against torch into the extension module _marshal.so, which links libvv.so.
+compiler against torch into the extension module _marshal.so, which links libvv.so; it needs
+Python's headers and a CUDA build of torch, and --lib-only leaves it out (C callers, and every
+Python entry point but the batch operators').
 """
 
 import argparse
@@ -85,12 +87,12 @@ def _link_marshal(obj):
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
 
 
-def build(force=False, jobs=None, verbose=False, extra=()):
+def build(force=False, jobs=None, verbose=False, extra=(), lib_only=False):
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
     with cf.ThreadPoolExecutor(jobs + 1) as ex:
-        marshal = ex.submit(_compile_marshal, force)
+        marshal = None if lib_only else ex.submit(_compile_marshal, force)
         results = list(ex.map(lambda s: _compile(s, force, list(extra)), srcs))
     objs = [o for o, _ in results]
     if verbose:
@@ -103,10 +105,16 @@ def build(force=False, jobs=None, verbose=False, extra=()):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    obj = marshal.result()
-    if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < max(
-            os.path.getmtime(obj), os.path.getmtime(LIB)):
-        _link_marshal(obj)
+    if lib_only:
+        return LIB
+    try:
+        obj = marshal.result()
+        if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < max(
+                os.path.getmtime(obj), os.path.getmtime(LIB)):
+            _link_marshal(obj)
+    except Exception as e:
+        raise RuntimeError(f"{os.path.basename(LIB)} is built, {os.path.basename(MARSHAL)} (the batch "
+                           "operators' Python side; --lib-only leaves it out) is not") from e
     return LIB
 
 
@@ -115,9 +123,10 @@ def main():
     ap.add_argument("--force", action="store_true")
     ap.add_argument("-j", type=int, default=None)
     ap.add_argument("-v", action="store_true", help="print ptxas resource usage")
+    ap.add_argument("--lib-only", action="store_true", help="libvv.so without _marshal")
     a = ap.parse_args()
     extra = ["-Xptxas", "-v"] if a.v else []
-    print(build(force=a.force or a.v, jobs=a.j, verbose=a.v, extra=extra))
+    print(build(force=a.force or a.v, jobs=a.j, verbose=a.v, extra=extra, lib_only=a.lib_only))
 
 
 if __name__ == "__main__":

@@ -1,0 +1,50 @@
+"""The extension module of the batch operators' binding: what needs it, and what does not (CPU only)."""
+
+import os
+import subprocess
+import sys
+
+import pytest
+
+pytest.importorskip("int4_blockwise_quantised_b200._vv")
+from int4_blockwise_quantised_b200 import build  # noqa: E402
+
+
+def copy_without_marshal(tmp_path):
+    """The package in a folder of its own, with libvv.so and without _marshal."""
+    pkg = tmp_path / os.path.basename(build.PKG)
+    pkg.mkdir()
+    for f in os.listdir(build.PKG):
+        if f.endswith(".py"):
+            (pkg / f).write_bytes(open(os.path.join(build.PKG, f), "rb").read())
+    os.symlink(build.LIB, pkg / "libvv.so")
+    os.symlink(build.INCLUDE, tmp_path / "include")
+    return pkg
+
+
+def test_other_operators_need_no_marshal(tmp_path):
+    pkg = copy_without_marshal(tmp_path)
+    code = f"""
+from {pkg.name} import _vv
+assert _vv.__file__.startswith({str(tmp_path)!r})
+assert _vv.vv_version() and _vv.vv_gqa_prefix_attn_workspace_size(2, 4, 2, 128, 100, 64) > 0
+for call in (lambda: _vv.vv_paged_plan(*[None] * 7), lambda: _vv.vv_logits_process(None)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_marshal" in str(e) and "build" in str(e)
+    else:
+        raise AssertionError("no ImportError")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_build_makes_the_library_without_marshal(monkeypatch):
+    def fail(*a):
+        raise RuntimeError("no host compiler")
+
+    monkeypatch.setattr(build, "_compile_marshal", fail)
+    assert build.build(lib_only=True) == build.LIB
+    with pytest.raises(RuntimeError, match="libvv.so is built"):
+        build.build()
