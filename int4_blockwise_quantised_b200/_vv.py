@@ -161,6 +161,8 @@ class _NoMarshal:
 
 try:
     from . import _marshal
+    if _marshal.torch_version != torch.__version__.split("+")[0]:
+        raise ImportError(f"made for torch {_marshal.torch_version}, this is {torch.__version__}")
     _marshal.set_error(VVError)
 except ImportError as e:  # the other operators need libvv.so alone
     _marshal = _NoMarshal(e)

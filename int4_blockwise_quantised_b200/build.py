@@ -5,24 +5,28 @@
 Each csrc/*.cu compiles to an object under _build/ (in parallel, skipped when up to date), then
 all objects link into int4_blockwise_quantised_b200/libvv.so with the CUDA runtime linked
 statically.  csrc/marshal.cpp (tensor arguments of the batch operators) compiles with the host
-compiler against torch into the extension module _marshal.so, which links libvv.so; it needs
+compiler against torch into the extension module _marshal (its file name carries the Python ABI; it is
+built again for another torch), which links libvv.so; it needs
 Python's headers and a CUDA build of torch, and --lib-only leaves it out (C callers, and every
 Python entry point but the batch operators').
 """
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvv.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -58,13 +62,19 @@ def _compile(src, force, extra):
     return obj, r.stderr
 
 
-def _compile_marshal(force):
-    src, obj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.o")
-    newest_dep = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "vv.h")))
-    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= newest_dep:
-        return obj
-    import sysconfig
+def _made_for():
+    """The Python and the torch that _marshal is compiled against (torch is not imported)."""
+    spec = importlib.util.find_spec("torch")
+    where = os.path.dirname(spec.origin) if spec else "none"
+    return f"{sysconfig.get_config_var('SOABI')} torch {importlib.metadata.version('torch')} {where}"
 
+
+def _compile_marshal(force):
+    src, obj, stamp = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.o"), os.path.join(BUILD, "marshal.txt")
+    newest_dep = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "vv.h")))
+    made_for = open(stamp).read() if os.path.exists(stamp) else None
+    if (not force and made_for == _made_for() and os.path.exists(obj) and os.path.getmtime(obj) >= newest_dep):
+        return obj
     from torch.utils import cpp_extension as ext
 
     inc = ext.include_paths() + [sysconfig.get_paths()["include"], "/usr/local/cuda/include"]
@@ -73,6 +83,8 @@ def _compile_marshal(force):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(_made_for())
     return obj
 
 
@@ -112,6 +124,9 @@ def build(force=False, jobs=None, verbose=False, extra=(), lib_only=False):
         if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < max(
                 os.path.getmtime(obj), os.path.getmtime(LIB)):
             _link_marshal(obj)
+        untagged = os.path.join(PKG, "_marshal.so")  # an earlier build's: every Python would load it
+        if os.path.exists(untagged):
+            os.remove(untagged)
     except Exception as e:
         raise RuntimeError(f"{os.path.basename(LIB)} is built, {os.path.basename(MARSHAL)} (the batch "
                            "operators' Python side; --lib-only leaves it out) is not") from e

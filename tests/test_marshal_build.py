@@ -3,6 +3,7 @@
 import os
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 
@@ -48,3 +49,43 @@ def test_build_makes_the_library_without_marshal(monkeypatch):
     assert build.build(lib_only=True) == build.LIB
     with pytest.raises(RuntimeError, match="libvv.so is built"):
         build.build()
+
+
+def test_module_is_of_this_python():
+    assert build.MARSHAL.endswith(sysconfig.get_config_var("EXT_SUFFIX")) and os.path.exists(build.MARSHAL)
+    assert not os.path.exists(os.path.join(build.PKG, "_marshal.so"))  # another Python would load it
+
+
+def test_module_is_built_again_for_another_torch(monkeypatch):
+    ran = []
+
+    def run(cmd, **k):
+        ran.append(cmd)
+        return subprocess.CompletedProcess(cmd, 1, "", "not run")
+
+    build._compile_marshal(False)
+    monkeypatch.setattr(build.subprocess, "run", run)
+    build._compile_marshal(False)
+    assert not ran  # up to date
+    monkeypatch.setattr(build, "_made_for", lambda: "another torch")
+    with pytest.raises(RuntimeError):
+        build._compile_marshal(False)
+    assert len(ran) == 1 and ran[0][0] == "g++"
+
+
+def test_module_made_for_another_torch_is_not_used(tmp_path):
+    pkg = copy_without_marshal(tmp_path)
+    os.symlink(build.MARSHAL, pkg / os.path.basename(build.MARSHAL))
+    code = f"""
+import torch
+torch.__version__ = "1.2.3+cu0"
+from {pkg.name} import _vv
+try:
+    _vv.vv_logits_process(None)
+except ImportError as e:
+    assert "1.2.3" in str(e)
+else:
+    raise AssertionError("no ImportError")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
