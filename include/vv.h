@@ -251,7 +251,8 @@ vv_status vv_paged_plan(const int32_t* lens, const int32_t* new_lens, int32_t B,
  * k_stride / v_stride elements apart (multiples of 8: the three parts of one fused projection can
  * be read in place); q_gain, k_gain device [D] of kv->dtype or NULL; positions device int32 [T];
  * slots device int64 [T]; q_out [T, Hq, D] with rows q_out_stride apart, q itself (same stride)
- * or apart from it.  A negative slot writes no key and value (padding); its q row is rotated all
+ * or apart from it, and apart from k's and v's rows (between them, as in a fused projection's own
+ * rows, counts as apart).  A negative slot writes no key and value (padding); its q row is rotated all
  * the same.  Slots of one call must differ (else which token a cell keeps is not defined).
  * Arithmetic in fp32, angles reduced in fp64, one rounding at the end; v is copied.
  * Requirements: D == 128, 1 <= Hq, Hkv <= 1024, 1 <= T < 2^31.  On the device, a slot past the

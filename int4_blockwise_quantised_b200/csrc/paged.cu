@@ -592,6 +592,17 @@ extern "C" vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const vo
   VV_CHECK_ARG((q0 == o0 && (T == 1 || q_stride == q_out_stride)) || q0 + q_bytes <= o0 ||
                    o0 + o_bytes <= q0,
                "vv_qk_rope_append: q_out must be q itself (same stride) or not overlap it");
+  // keys and values are read by other warps while q_out's rows are written: apart, or between its rows
+  // (parts of one fused buffer: the same stride)
+  auto meets = [&](const void* p, int64_t stride) {
+    const char* x = static_cast<const char*>(p);
+    const int64_t row = (int64_t)Hkv * D * 2, out_row = (int64_t)Hq * D * 2, s = stride * 2;
+    if (x + (T - 1) * s + row <= o0 || o0 + o_bytes <= x) return false;
+    if (T == 1 || stride != q_out_stride) return true;
+    const int64_t d = ((x - o0) % s + s) % s;  // from a row of q_out to the next row of p
+    return d < out_row || d + row > s;
+  };
+  VV_CHECK_ARG(!meets(k, k_stride) && !meets(v, v_stride), "vv_qk_rope_append: q_out must not overlap k and v");
   vv::RopeArgs a;
   a.q = static_cast<const char*>(q);
   a.k = static_cast<const char*>(k);
