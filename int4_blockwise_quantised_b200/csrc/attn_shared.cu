@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
   }
   // chunks of a sequence, per head: a sequence without keys has one empty chunk (its rows are
   // written by whoever holds it), a padding row none
-  auto chunks_of = [&](int len) { return len < 0 ? 0 : max(npre + (min(len, cap) + kChunk - 1) / kChunk, 1); };
+  // (unsigned: a length may be 2^31 - 1)
+  auto chunks_of = [&](int len) { return len < 0 ? 0 : max(npre + (int)(((unsigned)min(len, cap) + kChunk - 1) / kChunk), 1); };
   auto places_of = [&](int chunks) { return chunks ? (int64_t)chunks + kEnd : 0; };
   const int per = (a.B + kOwnThreads - 1) / kOwnThreads;
   const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);

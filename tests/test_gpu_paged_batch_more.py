@@ -29,3 +29,17 @@ def test_rope_append_in_place_within_a_fused_projection(vv, T):  # noqa: F811
     with pytest.raises(vv.VVError) as e:  # a head further on: over the first key head
         vv.vv_qk_rope_append(q, k, v, i32(pos), torch.tensor(slots).cuda(), kv, 1e6, out=fused[:, 1:1 + hq])
     assert e.value.code == vv.VV_ERR_INVALID_ARG
+
+
+def test_prefix_attn_of_as_many_keys_as_a_length_can_name(vv):  # noqa: F811
+    """2^31 - 1 keys, all of one page whose keys are equal: their mean is its value, their number in lse."""
+    k, v = (torch.full((1, 1, 16, 128), x, dtype=F16, device="cuda") for x in (0.25, 3.0))
+    kv, n = vv.PagedKV(k, v), 2 ** 31 - 1
+    q = torch.full((1, 1, 128), 0.5, dtype=F16, device="cuda")
+    table = torch.zeros((1, 2 ** 27), dtype=torch.int32, device="cuda")
+    ws = torch.empty(vv.vv_gqa_prefix_attn_workspace_size(1, 1, 1, 128, 0, 2 ** 31), dtype=torch.uint8, device="cuda")
+    lse = torch.empty((1, 1), device="cuda")
+    out = vv.vv_gqa_prefix_attn(q, None, None, kv, table, i32([n]), 0.125, ws, lse=lse)
+    vv.vv_sync_status()
+    assert torch.all(out == 3.0)
+    assert abs(lse.item() - (0.5 * 0.25 * 128 * 0.125 + math.log(n))) <= 1e-5  # 23.5 in fp32 steps
