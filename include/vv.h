@@ -278,7 +278,9 @@ vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const void* k, int6
  * A sequence without any key (or with every score -inf) gives zeros and lse -inf; own_lens[b] < 0
  * marks a padding row: its q is not used and its rows of out and lse are left as they were.
  * Scores, softmax and sums in fp32; the weights are rounded to the element type before they meet
- * V (as 2^x of at most 2^8: a relative half step each).
+ * V, since the tensor cores multiply 16-bit operands (vv_gqa_decode_attn keeps them in fp32): half
+ * a step of the type each (fp16 2^-11, bf16 2^-8, relative), but fp16 weights below 2^-20 of the
+ * sequence's largest are off by up to 2^-31 of it.
  * ws: device workspace of vv_gqa_prefix_attn_workspace_size(B, Hq, Hkv, D, prefix_len,
  * max_blocks * page_size) bytes, 16-byte aligned, of any contents; one sized for the largest batch,
  * prompt and table serves all smaller ones of the same heads; calls sharing one ws (captured ones

@@ -23,6 +23,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_shared.h"
 #include "attn_tc.cuh"
@@ -347,6 +348,10 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
         }
       }
     }
+    // fp16 weights are taken 2^14 larger than relative to the maximum, so that those down to 2^-28 keep
+    // all their bits; the reference carries it, and the join divides it out.  (2^15 would leave no room
+    // below fp16's 65504 for the rounding of a reference in the millions.)
+    constexpr float kHeadroom = std::is_same<T, __half>::value ? 14.f : 0.f;
     float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
           float mx = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[h], mx * a.c);
+          const float mn = fmaxf(m[h], fmaf(mx, a.c, -kHeadroom));
           const float ref = mn == -INFINITY ? 0.f : mn;  // nothing above -inf yet: all weights 0
           corr[h] = exp2_fast(m[h] - ref);
           m[h] = mn;

@@ -23,7 +23,8 @@
 // one group's exponentials run (128 a row and block: 1024 cycles of the special-function units)
 // the other loads, finds its maximum and stores.  O is rescaled only when a block's maximum
 // exceeds the running one by more than 2^8: weights stay below 2^8, and the same reference divides
-// them out.
+// them out.  fp16 weights are taken 2^6 larger still (at most 2^14), so that those down to 2^-20 of the
+// largest keep all their bits and smaller ones are off by at most 2^-31 of it.
 // The weights are rounded to the element type because the tensor cores multiply 16-bit operands;
 // their sum l is taken before that rounding.  The tile's partial rows (o, m, l) go to the workspace
 // in fp32; the join kernel puts the parts together.
@@ -36,6 +37,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_shared.h"
 #include "attn_tc.cuh"
@@ -54,6 +56,8 @@ constexpr int kThreads = 384;
 constexpr int kKStages = 3, kVStages = 2;  // V_j, P_j and S_j share the index j & 1
 constexpr int kTiles = 1 + kKStages + kVStages;
 constexpr float kRescale = 8.0f;
+template <typename T>
+constexpr float kHeadroom = std::is_same<T, __half>::value ? 6.0f : 0.0f;
 constexpr uint32_t kBarBytes = 256;
 constexpr int kOutRow = 132;  // floats per row of the output stage (conflict-free float4 columns)
 constexpr size_t kSmem = kTiles * kTile + kBarBytes + 2 * BM * 4 + 2 * BM * 8 + 1024;
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < 32; ++t) m4[t & 3] = fmaxf(m4[t & 3], __uint_as_float(sr[cc][t]));
       }
-      const float mb = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+      const float mb = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), c, -kHeadroom<T>);
       // the running reference after block j - 1, from the other group's warp of the same rows
       float m_prev = -INFINITY;
       if (j > 0) {

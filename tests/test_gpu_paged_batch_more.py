@@ -43,3 +43,49 @@ def test_prefix_attn_of_as_many_keys_as_a_length_can_name(vv):  # noqa: F811
     vv.vv_sync_status()
     assert torch.all(out == 3.0)
     assert abs(lse.item() - (0.5 * 0.25 * 128 * 0.125 + math.log(n))) <= 1e-5  # 23.5 in fp32 steps
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("B,P,n", [(1, 0, 16 * 3000), (3, 18 * 6 * 128, 0), (2, 4096, 16 * 500), (1, 20000, 0)])
+def test_prefix_attn_weights_far_below_the_largest(vv, dtype, B, P, n):  # noqa: F811
+    """Every 16th key takes all but e^-17.5 of a key's weight and has a value of zero: the result is what the
+    others carry together.  fp16 weights below 2^-20 of the largest are off by 2^-31 of it at most, larger ones
+    by half a step."""
+    hkv, hq = 8, 16
+    k16 = torch.zeros((16, 128), device="cuda")
+    k16[1:, 0] = -17.5
+    v16 = torch.full((16, 128), 1000.0, device="cuda")
+    v16[0] = 0
+    page = lambda x: x.expand(1, hkv, 16, 128).to(dtype).contiguous()  # noqa: E731
+    kv = vv.PagedKV(page(k16), page(v16))
+    pre = [x.repeat(P // 16, 1).expand(hkv, P, 128).to(dtype).contiguous() if P else None for x in (k16, v16)]
+    q = torch.zeros((B, hq, 128), dtype=dtype, device="cuda")
+    q[:, :, 0] = math.sqrt(128)
+    table = torch.zeros((B, max(1, n // 16)), dtype=torch.int32, device="cuda")
+    ws = torch.empty(vv.vv_gqa_prefix_attn_workspace_size(B, hq, hkv, 128, P, 16 * table.shape[1]), dtype=torch.uint8, device="cuda")
+    lse = torch.empty((B, hq), device="cuda")
+    scale = 1 / math.sqrt(128)
+    out = vv.vv_gqa_prefix_attn(q, *pre, kv, table, i32([n] * B), scale, ws, lse=lse)
+    vv.vv_sync_status()
+    w = math.exp(-17.5 * q[0, 0, 0].item() * scale)
+    y, total = 1000 * 15 * w / (1 + 15 * w), 1 + 15 * w
+    u = u_of(dtype)
+    bound = 2 * u * y + 2.0 ** -19 * y + (1000 * 15 * 2.0 ** -31 + 2.0 ** -25 if dtype == F16 else 0.0)
+    assert np.max(np.abs(host(out) - y)) <= bound, (out.flatten()[:4].tolist(), y, bound)
+    assert np.max(np.abs(host(lse) - math.log((P + n) / 16 * total))) <= 1e-5
+
+
+@pytest.mark.parametrize("B,P,n", [(1, 0, 500), (4, 1500, 40)])
+def test_prefix_attn_scores_of_millions(vv, B, P, n):  # noqa: F811
+    """One key takes all, whatever the score's size in fp32: no weight passes the type's largest value."""
+    c = attn_case(vv, B, 12, 2, P, [n] * B, 16, F16, seed=31)
+    for t in (c["kpre"], c["kv"].k):
+        if t is not None:
+            t[..., 0] = torch.randperm(t[..., 0].numel(), device="cuda").view(t[..., 0].shape).to(F16) * 8
+    c["q"][:, :, 0] = 2000.0
+    c["q"][:, 1::2, 0] *= -1
+    c["qh"], c["kph"] = host(c["q"]), host(c["kv"].k)
+    c["kpreh"] = host(c["kpre"]) if P else None
+    out, lse = attn_run(vv, c)
+    vv.vv_sync_status()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
