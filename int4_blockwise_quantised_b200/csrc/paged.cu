@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 // one or two on their way (cp.async.bulk into a ring of its own, a token's heads of one kind are
 // contiguous), whatever its registers and without a barrier between warps.  Half a warp turns one
 // head row; a lane holds four elements and their partners, so that each is read and converted once.
-// A token's angles are found once per unit, two a lane: the turns pos * theta^(-2i/128) / 2 pi
+// A token's angles are found once per unit, two a lane: the quarter turns pos * theta^(-2i/128) * 2 / pi
 // reduced to [-1/2, 1/2] in 64 bits (in 32 bits a position of 10^6 would lose the angle's second
 // digit), then sine and cosine of the remainder in 32 bits.
 constexpr int kHeadDim = 128;
@@ -292,7 +292,7 @@ struct RopeArgs {
   int T, Hq, Hkv, ps;
   int heads, parts;  // heads per unit; units per token
   float eps;
-  double turns[kHeadDim / 2];  // theta^(-2i/D) / (2 pi)
+  double quarters[kHeadDim / 2];  // quarter turns a position: theta^(-2i/D) 2 / pi
 };
 
 template <typename T>
@@ -342,6 +342,25 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
+// Sine and cosine of z quarter turns, |z| <= 1/2: polynomials in w = z^2, interpolated at four Chebyshev
+// nodes of [0, 1/4] to sin(pi z / 2) / z and (cos(pi z / 2) - 1) / w.  Right to 2^-22.8 of the value,
+// however small it is; the hardware's fast sine is off by up to 2^-21, a third of the sine by which
+// the slowest pair of theta 10^6 turns the token at position 1.
+__device__ __forceinline__ void sincos2(f32x2 z, f32x2& sn, f32x2& cn) {
+  auto both = [](float x) { return pair(x, x); };
+  const f32x2 w = mul2(z, z);
+  const f32x2 p = fma2(fma2(fma2(both(-0.00460214913f), w, both(0.0796802193f)), w, both(-0.645963490f)), w, both(1.57079637f));
+  const f32x2 q = fma2(fma2(fma2(both(9.06739908e-4f), w, both(-0.0208615288f)), w, both(0.253669411f)), w, both(-1.23370051f));
+  sn = mul2(p, z);
+  cn = fma2(q, w, both(1.f));
+}
+// (cosine, sine) of n quarter turns more, n a whole number: its last two bits, where 2^52 + 2^51 puts them
+__device__ __forceinline__ float2 quadrant(double n, float c, float s) {
+  const unsigned q = (unsigned)__double2loint(n + 6755399441055744.0);
+  const unsigned x = __float_as_uint(q & 1 ? s : c), y = __float_as_uint(q & 1 ? c : s);
+  return make_float2(__uint_as_float(x ^ ((q + 1) << 30 & 0x80000000u)), __uint_as_float(y ^ (q << 30 & 0x80000000u)));
+}
+
 template <typename T, bool GAINS>
 __global__ void __launch_bounds__(RopeShape<GAINS>::kWarps * 32, 2)
     qk_rope_append_kernel(const __grid_constant__ RopeArgs a) {
@@ -379,7 +398,7 @@ __global__ void __launch_bounds__(RopeShape<GAINS>::kWarps * 32, 2)
   for (int i = 0; i < kRopeStages; ++i) copy(u0 + i * step, i);
 
   const int c = lane & 15;  // elements 4c .. 4c + 3 of a row and their partners; 16-byte piece of a value row
-  const double f0 = a.turns[lane], f1 = a.turns[lane + 32];
+  const double f0 = a.quarters[lane], f1 = a.quarters[lane + 32];
   int pos = 0;
   int64_t slot = -1;
   if (u0 < units) {
@@ -391,12 +410,12 @@ __global__ void __launch_bounds__(RopeShape<GAINS>::kWarps * 32, 2)
   for (int64_t u = u0; u < units; u += step) {
     const int t = (int)(u / a.parts), h0 = (int)(u - (int64_t)t * a.parts) * a.heads, nh = min(a.heads, n_heads - h0);
     {
-      const double x0 = (double)pos * f0, x1 = (double)pos * f1;
-      // |remainder| <= pi: the fast sine and cosine are off by at most 2^-21 there, far below a half
-      // step of the 16-bit results
-      const float kTwoPi = 6.28318530717958648f, r0 = kTwoPi * (float)(x0 - rint(x0)), r1 = kTwoPi * (float)(x1 - rint(x1));
-      cs[lane] = make_float2(__cosf(r0), __sinf(r0));
-      cs[lane + 32] = make_float2(__cosf(r1), __sinf(r1));
+      const double x0 = (double)pos * f0, x1 = (double)pos * f1, n0 = rint(x0), n1 = rint(x1);
+      f32x2 sn, cn;
+      sincos2(pair((float)(x0 - n0), (float)(x1 - n1)), sn, cn);
+      const float2 s = unpair(sn), c = unpair(cn);
+      cs[lane] = quadrant(n0, c.x, s.x);
+      cs[lane + 32] = quadrant(n1, c.y, s.y);
     }
     int64_t at = -1;  // byte offset of the token's cell in the pool
     if (slot >= a.n_slots) {
@@ -627,11 +646,10 @@ extern "C" vv_status vv_qk_rope_append(const void* q, int64_t q_stride, const vo
   a.Hkv = Hkv;
   a.ps = kv->page_size;
   a.eps = eps;
-  const double kTwoPi = 6.283185307179586476925286766559;
-  a.turns[0] = 1.0 / kTwoPi;
+  a.quarters[0] = 2.0 / 3.14159265358979323846;
   for (int n = 1; n < D / 2; n *= 2) {  // theta^(-2 i / D) from the powers of i's bits
     const double f = std::pow((double)theta, -2.0 * n / D);
-    for (int i = 0; i < n; ++i) a.turns[n + i] = a.turns[i] * f;
+    for (int i = 0; i < n; ++i) a.quarters[n + i] = a.quarters[i] * f;
   }
   // a token in as few units of at most 18 heads as there are warps for, in smaller ones (an even
   // number of heads, two rows at a time) when tokens are few

@@ -89,3 +89,48 @@ def test_prefix_attn_scores_of_millions(vv, B, P, n):  # noqa: F811
     out, lse = attn_run(vv, c)
     vv.vv_sync_status()
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("gains", [False, True])
+def test_rope_append_small_angles(vv, dtype, gains):  # noqa: F811
+    """Where a partner is zero the rotated value is x cos or x sin alone, and its error one rounding: the
+    angle (reduced in fp64) is off by 2^-24 of itself, up to 2 pi 2^-26 where it is reduced, a sine and
+    cosine by 2 of their last places (2^-24 below 1), products and a norm by 2^-20 of the value."""
+    T, hq, hkv, theta = 64, 4, 2, 1e6
+    x, xh = values((T, hq + 2 * hkv, 128), dtype, 21)
+    x[:, ::2, 64:] = 0
+    x[:, 1::2, :64] = 0
+    xh = host(x)
+    g, gh = values((128,), dtype, 22) if gains else (None, None)
+    kv, kp, vp = pools(vv, T // 16, hkv, 16, dtype, 23)
+    pos = np.concatenate([np.arange(-8, 24), 10 ** np.arange(8), 1000 + np.arange(24)])
+    slots = np.arange(T)
+    out = vv.vv_qk_rope_append(x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], i32(pos), torch.tensor(slots).cuda(), kv,
+                               theta, q_gain=g, k_gain=g)
+    vv.vv_sync_status()
+    yq, yk, _ = obatch.qk_rope_append(xh[:, :hq], xh[:, hq:hq + hkv], xh[:, hq + hkv:], pos, slots, kp, vp, theta, gh, gh)
+    angle = np.abs(pos[:, None].astype(np.float64) * theta ** (-2.0 * np.arange(64) / 128))
+    angle = np.minimum(np.concatenate([angle, angle], -1), 1.0)[:, None]
+
+    def bound(y, heads):
+        n = obatch.ops.rmsnorm(heads, gh, 1e-6) if gains else heads
+        a = np.abs(n) + np.abs(np.roll(n, 64, axis=-1))
+        return (u_of(dtype) + 2.0 ** -20) * np.abs(y) + 2.0 ** -22 * a * angle + (2.0 ** -25 if dtype == F16 else 0.0)
+
+    assert np.all(np.abs(host(out) - yq) <= bound(yq, xh[:, :hq]))
+    cells = lambda pages: pages.swapaxes(1, 2).reshape(T, hkv, 128)  # noqa: E731
+    got, want = cells(host(kv.k)), cells(yk)
+    assert np.all(np.abs(got - want) <= bound(want, xh[:, hq:hq + hkv]))
+
+
+@pytest.mark.parametrize("theta", [1e-9, 0.5, 3.4e38])
+def test_rope_append_any_theta_rotates(vv, theta):  # noqa: F811
+    """Angles beyond what 64 bits resolve still turn by some angle: a pair keeps its length."""
+    x, xh = values((40, 3, 128), F16, 41)
+    kv, _, _ = pools(vv, 3, 1, 16, F16, 42)
+    pos = [0, 1, -1, 2 ** 31 - 1, -2 ** 31] * 8
+    out = vv.vv_qk_rope_append(x[:, :1], x[:, 1:2], x[:, 2:], i32(pos), torch.arange(40, device="cuda"), kv, theta)
+    vv.vv_sync_status()
+    length = lambda y: np.hypot(y[..., :64], y[..., 64:])  # noqa: E731
+    assert np.all(np.abs(length(host(out)) - length(xh[:, :1])) <= 2 * u_of(F16) * length(xh[:, :1]) + 2.0 ** -24)
