@@ -80,6 +80,11 @@ struct Args {
     if (x != (int32_t)x) refuse("%s: %s = %lld does not fit 32 bits", who, name, (long long)x);
     return x;
   }
+  bool truth() {
+    const int x = PyObject_IsTrue(next());
+    if (x < 0) throw Refused();
+    return x == 1;
+  }
   double number() {
     const double x = PyFloat_AsDouble(next());
     if (x == -1.0 && PyErr_Occurred()) throw Refused();
@@ -337,7 +342,7 @@ PyObject* logits_process(Args& a) {
   const at::Tensor *ids = a.tensor_or_none("bias_ids"), *vals = a.tensor_or_none("bias_vals"),
                    *offs = a.tensor_or_none("bias_offsets");
   const at::Tensor* mask = a.tensor_or_none("mask");
-  const bool argmax = PyObject_IsTrue(a.next()) == 1;
+  const bool argmax = a.truth();
   const at::Tensor* given = a.tensor_or_none("out");
   const auto type = x.scalar_type();
   if (x.dim() != 2 || (type != kF32 && type != at::kHalf && type != at::kBFloat16))

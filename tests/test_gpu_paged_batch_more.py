@@ -134,3 +134,11 @@ def test_rope_append_any_theta_rotates(vv, theta):  # noqa: F811
     vv.vv_sync_status()
     length = lambda y: np.hypot(y[..., :64], y[..., 64:])  # noqa: E731
     assert np.all(np.abs(length(host(out)) - length(xh[:, :1])) <= 2 * u_of(F16) * length(xh[:, :1]) + 2.0 ** -24)
+
+
+def test_logits_argmax_that_is_neither_true_nor_false(vv):  # noqa: F811
+    x = torch.zeros((2, 100), device="cuda")
+    ws = torch.zeros(vv.vv_logits_process_workspace_size(2), dtype=torch.uint8, device="cuda")
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        vv.vv_logits_process(x, ws, argmax=torch.ones(2))
+    assert vv.vv_logits_process(x, ws, argmax=torch.ones(1))[1].tolist() == [0, 0]
