@@ -299,8 +299,9 @@ def vv_lm_head_argmax(x, gamma, w_lm, eps, ws, logits=True, stream=None):
 # into pointers by the extension module _marshal.
 def _on(stream, function, *args):
     """function(*args) with `stream` (a torch.cuda.Stream) and its device current."""
-    if stream.device != args[0].device:
-        raise VVError(VV_ERR_INVALID_ARG, f"stream of {stream.device}, tensors on {args[0].device}")
+    device = getattr(args[0], "device", None)  # None: not a tensor
+    if stream.device != device:
+        raise VVError(VV_ERR_INVALID_ARG, f"stream of {stream.device}, tensors on {device}")
     with torch.cuda.stream(stream):
         return function(*args)
 
