@@ -18,6 +18,7 @@ import hashlib
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -844,10 +845,27 @@ def phase_breakdown(st, L):
     return {k: round(v / 1e3, 1) for k, v in out.items()}
 
 
+def source_sha(source):
+    """Hash of a kernel's source with the csrc headers it includes, directly or through each other
+    (vv_internal.h, which has no device code, and the C ABI's header leave a kernel as it is)."""
+    todo, seen = [os.path.join(ROOT, source)], []
+    while todo:
+        p = os.path.normpath(todo.pop(0))
+        if p in seen or not os.path.exists(p):
+            continue
+        seen.append(p)
+        names = re.findall(r'^\s*#include\s+"([^"/]+)"', open(p).read(), flags=re.M)
+        todo += [os.path.join(os.path.dirname(p), n) for n in names if n != "vv_internal.h"]
+    h = hashlib.sha256()
+    for p in seen[:1] + sorted(seen[1:]):
+        h.update(open(p, "rb").read())
+    return h.hexdigest()[:16]
+
+
 def traffic_for(kernel, workload=None):
     """DRAM bytes per launch from the committed ncu summary (entry "kernel/workload", or "kernel"
     when no workload is named), or None when there is no capture of that workload or the
-    kernel's source changed since the counters were taken."""
+    kernel's source, headers included, changed since the counters were taken."""
     p = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(p):
         return None
@@ -855,9 +873,7 @@ def traffic_for(kernel, workload=None):
     d = tab.get(f"{kernel}/{workload}") if workload else tab.get(kernel)
     if not d:
         return None
-    src = os.path.join(ROOT, d["source"])
-    h = hashlib.sha256(open(src, "rb").read()).hexdigest()[:16] if os.path.exists(src) else None
-    return d["dram_bytes_per_launch"] if h == d.get("source_sha") else None
+    return d["dram_bytes_per_launch"] if source_sha(d["source"]) == d.get("source_sha") else None
 
 
 # ------------------------------------------------------------------------------ reference arm
