@@ -142,3 +142,53 @@ def test_logits_argmax_that_is_neither_true_nor_false(vv):  # noqa: F811
     with pytest.raises(RuntimeError, match="ambiguous"):
         vv.vv_logits_process(x, ws, argmax=torch.ones(2))
     assert vv.vv_logits_process(x, ws, argmax=torch.ones(1))[1].tolist() == [0, 0]
+
+
+def test_prefix_attn_smaller_batches_on_the_largest_ones_workspace(vv):  # noqa: F811
+    """Sequences finish and a shorter prompt follows: the workspace of the largest call still serves, with the
+    bits of a workspace of the call's own."""
+    B, P, width = 16, 4096, 20
+    ws = torch.empty(vv.vv_gqa_prefix_attn_workspace_size(B, 12, 2, 128, P, width * 16), dtype=torch.uint8, device="cuda")
+    for b, p in ((16, 4096), (16, 3968), (11, 4096), (11, 2000), (2, 4096), (2, 130), (1, 4096), (3, 0)):
+        c = attn_case(vv, b, 12, 2, p, [(17 * i) % 300 for i in range(b)], 16, F16, seed=b + p, max_blocks=width)
+        out, lse = attn_run(vv, c, ws)
+        own, own_lse = attn_run(vv, c)
+        vv.vv_sync_status()
+        assert torch.equal(out, own) and torch.equal(lse, own_lse)
+        if p <= 2000:
+            attn_check(c, out, lse)
+
+
+@pytest.mark.parametrize("B,hq,hkv,P", [(65535, 1, 1, 200), (65535, 4, 1, 0), (3, 1024, 1024, 300), (1, 16384, 1024, 130)])
+def test_prefix_attn_largest_batches_and_head_counts(vv, B, hq, hkv, P):  # noqa: F811
+    """Rows at both ends of the range and between, against the formula in 64 bits."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B + hq)
+    normal = lambda *s: torch.randn(s, generator=g, device="cuda").to(F16)  # noqa: E731
+    q, kv = normal(B, hq, 128), vv.PagedKV(normal(5, hkv, 16, 128), normal(5, hkv, 16, 128))
+    pre = [normal(hkv, P, 128) if P else None for _ in range(2)]
+    lens = torch.randint(-1, 40, (B,), generator=g, device="cuda", dtype=torch.int32)
+    lens[0], lens[-1] = 39, 17
+    tables = torch.randint(0, 5, (B, 3), generator=g, device="cuda", dtype=torch.int32)
+    ws = torch.empty(vv.vv_gqa_prefix_attn_workspace_size(B, hq, hkv, 128, P, 48), dtype=torch.uint8, device="cuda")
+    lse = torch.full((B, hq), 77.0, device="cuda")
+    out = vv.vv_gqa_prefix_attn(q, *pre, kv, tables, lens, 1 / math.sqrt(128), ws, lse=lse)
+    vv.vv_sync_status()
+    u = u_of(F16)
+    for b in sorted({0, 1, 127, 128, B // 2, B - 1} & set(range(B))):
+        n = int(lens[b])
+        for h in sorted({0, hq // 2, hq - 1}):
+            if n < 0:
+                assert lse[b, h] == 77.0
+                continue
+            keys, vals = (torch.cat(([p[h * hkv // hq]] if P else []) + [x[int(t), h * hkv // hq] for t in tables[b]])[: P + n].double()
+                          for p, x in zip(pre, (kv.k, kv.v)))
+            if P + n == 0:
+                assert torch.all(out[b, h] == 0) and torch.isneginf(lse[b, h])
+                continue
+            s = keys @ q[b, h].double() / math.sqrt(128)
+            w = torch.softmax(s, 0)
+            y, mean = w @ vals, w @ vals.abs()
+            # as in test_gpu_paged_batch: one rounding of the result, one of each weight, scores in fp32
+            assert torch.all((out[b, h].double() - y).abs() <= u * y.abs() + (u + 2.0 ** -13) * mean + 2.0 ** -24)
+            assert abs(lse[b, h].item() - torch.logsumexp(s, 0).item()) <= 1e-4
