@@ -181,8 +181,8 @@ vv_status vv_lm_head_argmax(const float* x, const uint16_t* gamma, const uint16_
 /* ---------------------------------------------------------------------------------------------
  * A batch that continues one shared prompt ([STATUS]: several contexts stepped alongside each
  * other; [BITNET] decoder_init / decoder_step).  Several transcripts of one recording, or several
- * questions about it, decode together from the prompt that one vv_decoder_init_seq (or any other
- * prefill) left in a contiguous cache slice [Hkv, cap, D]; what each sequence adds lives in pages
+ * questions about it, decode together from the prompt that one vv_decoder_init_seq (fp16 caches; or any
+ * other prefill) left in a contiguous cache slice [Hkv, cap, D]; what each sequence adds lives in pages
  * of a common pool.  A step of such a batch, per layer, with the caller's projections between:
  *   vv_paged_plan      once a step: pages, slots, positions and row offsets of the new tokens
  *   vv_qk_rope_append  per layer: head norms, rotation, keys and values into their pages
@@ -332,6 +332,8 @@ typedef struct vv_logits_rules {
 
 /* logits and out: device [B, V] of `dtype` (VV_F32, VV_F16 or VV_BF16), rows the given number of
  * elements apart; out may be the logits themselves (same stride), else it must not overlap them.
+ * Rows of both that begin on 16 bytes move 16 bytes at a time, others (an odd V packed, a slice of a
+ * wider buffer) element by element, up to twice as slow for 16-bit logits.
  * argmax device int32 [B] or NULL.  Ids outside [0, V) in tokens and bias_ids are passed over
  * (padding); lengths outside [0, max_tokens] and offsets outside [0, n_bias] are cut to that
  * range, and record VV_ERR_RANGE.

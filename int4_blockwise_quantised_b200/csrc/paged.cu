@@ -28,8 +28,8 @@ namespace {
 // lengths are a few KB, in L2 after the first CTA), keeps the exclusive sums of tokens and pages
 // in shared memory and then takes its share of the requests, of the new pages and of the tokens;
 // a token or page finds its request by bisection in those sums.  A step of a small batch is one
-// CTA: what it costs is the latency of load, scan, bisection and store, not bytes (5.3 us for 32
-// requests, 5.8 for 301; 4096 requests with 778k tokens, 9.5 MB: 12.4 us).
+// CTA: what it costs is the latency of load, scan, bisection and store, not bytes (5.0 us for 32
+// requests, 5.9 for 301; 4096 requests with 778k tokens, 9.5 MB: 12.4 us).
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 16384;  // three int32 per request in shared memory (192 KB)
 
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
 //   (x_i, x_{i+64}) <- (x_i c - x_{i+64} s, x_{i+64} c + x_i s),  angle = pos * theta^(-2i/128)
 //
 // Bound by HBM: every head row is read once and written once (512 bytes for 128 elements): 50001
-// tokens of 28 + 4 + 4 heads take 153 to 166 us (6.0 to 5.6 TB/s, by where the tensors lie); with
-// norms the instructions count too, 158 us and 21.7 us for 4530 such tokens (3.8 TB/s); 16 tokens of
-// 12 + 2 + 2 heads take 2.9 us.
+// tokens of 28 + 4 + 4 heads take 154 us in a replayed graph (6.0 TB/s), 159 to 167 among eager calls;
+// with norms the instructions count too, 161 us, and 22.0 us for 4530 such tokens (3.8 TB/s); 16 tokens of
+// 12 + 2 + 2 heads take 3.0 us.
 // A unit is one token's heads, or a part of them; a warp works alone on its units and has the next
 // one or two on their way (cp.async.bulk into a ring of its own, a token's heads of one kind are
 // contiguous), whatever its registers and without a barrier between warps.  Half a warp turns one
@@ -267,8 +267,8 @@ constexpr int kHeadDim = 128;
 constexpr int kRopeHeads = 18;  // most heads of a unit, 4.5 KB
 // With norms a row takes half as many instructions again: eight warps per CTA (two CTAs per SM) and one
 // unit on its way beside the one in work.  Without, as many warps ask memory for more than it gives
-// in good order: 50001 tokens of 28 + 4 + 4 heads take 169 us with eight, 170 with six, 153 with five
-// and 160 with four; with norms 158 with eight and 225 with five.
+// in good order: 50001 tokens of 28 + 4 + 4 heads take 171 us with eight, 170 with six, 154 with five
+// and 161 with four; with norms 161 with eight, 188 with six and 225 with five.
 template <bool GAINS>
 struct RopeShape {
   static constexpr int kWarps = GAINS ? 8 : 5;
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(RopeShape<GAINS>::kWarps * 32, 2)
       }
     };
     // rows from .. to - 1 of the unit, two at a time, row r to dst(r)
-    // (two iterations at once send memory the same requests in bursts: 157 us instead of 153)
+    // (two iterations at once send memory the same requests in bursts: 2% slower without norms)
     auto turn = [&](int from, int to, bool norm, auto&& dst) {
       const unsigned char* in = ring + st * unit_bytes + c * 8;
 #pragma unroll 1
