@@ -27,6 +27,7 @@
 
 #include "attn_shared.h"
 #include "attn_tc.cuh"
+#include "pack16.cuh"
 #include "vv_device.cuh"
 #include "vv_internal.h"
 
@@ -87,18 +88,6 @@ struct SharedAttnArgs {
 };
 
 template <typename T>
-__device__ __forceinline__ uint32_t pack_pair(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack_pair<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack_pair<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
 __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -120,12 +109,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ float exp2_fast(float x) {  // -inf -> 0; its error is far below a half step of T
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Copies a chunk of K or of V: both halves of 64 dimensions, 16 rows each.
 __device__ __forceinline__ void tma_chunk(uint32_t dst, const CUtensorMap* tm, int token, int head, int page,
                                           uint64_t* bar) {
@@ -185,7 +168,7 @@ __device__ __forceinline__ void absorb(Joined& r, int n, int lane, F&& part) {
       if (k0 + k < n) v[k] = *reinterpret_cast<const float4*>(part(k0 + k) + lane * 4);
     }
     const float mn = fmaxf(r.m, warp_max(ml.x)), ref = mn == -INFINITY ? 0.f : mn;
-    const float w0 = exp2_fast(r.m - ref), w = exp2_fast(ml.x - ref);
+    const float w0 = tc::ex2_approx(r.m - ref), w = tc::ex2_approx(ml.x - ref);
     r.m = mn;
     r.l = r.l * w0 + warp_sum(w * ml.y);
     r.o = make_float4(r.o.x * w0, r.o.y * w0, r.o.z * w0, r.o.w * w0);
@@ -402,13 +385,13 @@ __global__ void __launch_bounds__(kOwnThreads, 1)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float mn = fmaxf(m[h], fmaf(mx, a.c, -kHeadroom));
           const float ref = mn == -INFINITY ? 0.f : mn;  // nothing above -inf yet: all weights 0
-          corr[h] = exp2_fast(m[h] - ref);
+          corr[h] = tc::ex2_approx(m[h] - ref);
           m[h] = mn;
-          const float w0 = exp2_fast(fmaf(sc[0][2 * h], a.c, -ref)), w1 = exp2_fast(fmaf(sc[0][2 * h + 1], a.c, -ref));
-          const float w2 = exp2_fast(fmaf(sc[1][2 * h], a.c, -ref)), w3 = exp2_fast(fmaf(sc[1][2 * h + 1], a.c, -ref));
+          const float w0 = tc::ex2_approx(fmaf(sc[0][2 * h], a.c, -ref)), w1 = tc::ex2_approx(fmaf(sc[0][2 * h + 1], a.c, -ref));
+          const float w2 = tc::ex2_approx(fmaf(sc[1][2 * h], a.c, -ref)), w3 = tc::ex2_approx(fmaf(sc[1][2 * h + 1], a.c, -ref));
           l[h] = l[h] * corr[h] + ((w0 + w1) + (w2 + w3));
-          p[h] = pack_pair<T>(w0, w1);
-          p[h + 2] = pack_pair<T>(w2, w3);
+          p[h] = pack2<T>(w0, w1);
+          p[h + 2] = pack2<T>(w2, w3);
         }
         if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
@@ -504,7 +487,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   // l is 0 where no key has a weight; a NaN score makes l NaN and goes on to the result
   const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
   T* dst = static_cast<T*>(a.out) + (int64_t)b * a.out_stride + h * D + lane * 4;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_pair<T>(r.o.x * inv, r.o.y * inv), pack_pair<T>(r.o.z * inv, r.o.w * inv));
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(r.o.x * inv, r.o.y * inv), pack2<T>(r.o.z * inv, r.o.w * inv));
   if (a.lse && lane == 0) a.lse[(int64_t)b * Hq + h] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
 }
 

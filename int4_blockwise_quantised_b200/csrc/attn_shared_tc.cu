@@ -43,6 +43,7 @@
 
 #include "attn_shared.h"
 #include "attn_tc.cuh"
+#include "pack16.cuh"
 #include "vv_device.cuh"
 #include "vv_internal.h"
 
@@ -71,19 +72,6 @@ constexpr uint32_t idesc(bool b_mn) {
   const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
   return (1u << 4) | (f << 7) | (f << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(BN >> 3) << 17) |
          ((uint32_t)(BM >> 4) << 24);
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack_w(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack_w<__half>(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack_w<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 struct KvMaps {
@@ -320,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float e1 = ex2_approx(fmaf(__uint_as_float(sr[hh * 2 + (t >> 5)][(t & 31) + 1]), c, -ref));
           ls0 += e0;
           ls1 += e1;
-          pp[t >> 1] = pack_w<T>(e0, e1);
+          pp[t >> 1] = pack2<T>(e0, e1);
         }
         tmem_st32(tP(s) + lane_off + (uint32_t)(hh * 32), pp);
       }

@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "pack16.cuh"
 #include "vv_device.cuh"
 #include "vv_internal.h"
 
@@ -294,29 +295,6 @@ struct RopeArgs {
   float eps;
   double quarters[kHeadDim / 2];  // quarter turns a position: theta^(-2i/D) 2 / pi
 };
-
-template <typename T>
-__device__ __forceinline__ float2 unpack2(uint32_t w);
-template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-}
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float2 x);
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float2 x) {
-  const __half2 h = __floats2half2_rn(x.x, x.y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float2 x) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // Two fp32 numbers in one register pair: sm_100 multiplies and adds both in one instruction.
 using f32x2 = unsigned long long;
