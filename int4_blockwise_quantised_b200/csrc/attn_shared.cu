@@ -15,7 +15,7 @@
 // head's parts are a dozen dependent reads.
 //
 // Measured: 2 x (1024 + at most 64) keys, 12 / 2 heads: 8.4 us; 16 x (4530 + 257): 12.8 us; 48 x (32768 +
-// 1024), 28 / 4 heads: 47 us (23 GFLOP, 125 MB); 23 x 4785 without a prompt: 23.9 us (92 MB, 3.9 TB/s).
+// 1024), 28 / 4 heads: 46 us (23 GFLOP, 125 MB); 23 x 4785 without a prompt: 23.9 us (92 MB, 3.9 TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
